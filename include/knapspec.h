@@ -263,6 +263,123 @@ KS_API ks_status ks_attention_bf16(const void* q, const void* k_layer, const voi
                                    int32_t* status, ks_stream_t stream);
 
 /*
+ * The paged key/value cache of a draft-and-verify loop (the paper has no
+ * counterpart: the solve reads one request's contiguous cache; a server that
+ * drafts with the chosen layer set and verifies with the full model keeps many
+ * requests' keys and values in pages).  Three calls per step: ks_page_plan
+ * once, then per layer ks_rope_append_bf16 and ks_paged_attention_bf16.
+ *
+ * A pool is one layer's pages (device, bf16, 16-byte aligned):
+ * k_pages, v_pages [n_pages][page_size][n_kv_heads][head_dim], keys rotated.
+ * Position p of request b lies in page block_table[b][p / page_size], row
+ * p % page_size; its slot is page * page_size + row.  head_dim is 64 or 128,
+ * page_size a multiple of 8, n_pages * page_size at most 2^31 - 256
+ * (else KS_ERR_UNSUPPORTED).  A step's tokens are packed: request b's new
+ * tokens are rows cu_new[b] .. cu_new[b+1]-1, at the positions
+ * kv_len[b] - new .. kv_len[b] - 1.  At most 16384 requests.
+ * status: device [1] word (the caller zeroes it) or NULL; the first error wins.
+ */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} ks_page_pool;
+
+/*
+ * A step's layout from the requests' lengths, on the device.  Request b holds
+ * ctx_len[b] tokens (their pages are in row b of block_table) and appends
+ * new_len[b] (0 is an idle request).  Where its last page is full it takes the
+ * next pages of free_pages (device [n_free] page ids), requests in order:
+ *   cu_new[b]    = new_len[0] + .. + new_len[b-1]          (device [B+1])
+ *   kv_len[b]    = ctx_len[b] + new_len[b]                 (device [B])
+ *   block_table  = the taken pages' entries written        (device [B][max_blocks])
+ *   positions[i] = position of packed token i              (device [max_tokens])
+ *   slots[i]     = its slot                                (device [max_tokens])
+ *   n_taken[0]   = pages taken from the front of free_pages (device [1])
+ * Rows of positions and slots behind the last token get -1; entries of
+ * block_table that are not taken now keep what they hold, so the call may be
+ * repeated with the same lengths.  No output may overlap an input, block_table
+ * apart.  A negative length, a request longer than max_blocks pages or more
+ * than max_tokens tokens is KS_ERR_INVALID_ARG in status, too few free pages
+ * KS_ERR_WORKSPACE; the step is then empty (cu_new, kv_len and n_taken 0,
+ * positions and slots -1, block_table as it was).  A page id outside
+ * 0 .. n_pages-1 (in free_pages, or in the entry that holds a new token) gives
+ * its tokens slot -1 and KS_ERR_INVALID_ARG; the entry then holds -1 if it
+ * was taken now.
+ */
+KS_API ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
+                              const int32_t* free_pages, int32_t n_free, int32_t n_pages,
+                              int32_t page_size, int32_t* block_table, int32_t max_blocks,
+                              int32_t max_tokens, int32_t* cu_new, int32_t* kv_len,
+                              int32_t* positions, int32_t* slots, int32_t* n_taken,
+                              int32_t* status, ks_stream_t stream);
+
+/*
+ * Rotary positions on a step's queries and keys, and its keys and values into
+ * their pages, in one pass: with theta_j = rope_base^(-2j/head_dim) and p =
+ * positions[i], q_out[i] = RoPE_p(q[i]), slot slots[i] of the pool = RoPE_p(k[i])
+ * and v[i] (rotate-half: elements j and j + head_dim/2 are a pair).  Angles
+ * are fp64, the rotation fp32, rounded once to bf16.
+ * q [n_tokens][n_q_heads][head_dim], k, v [n_tokens][n_kv_heads][head_dim]:
+ * device bf16, token rows q_stride / k_stride / v_stride elements apart
+ * (multiples of 8, at least a row), so one fused projection's output can be
+ * read in place; q_out [n_tokens][n_q_heads][head_dim] contiguous.  q_out may
+ * be q itself where q is contiguous; no other overlap is allowed.  q and q_out
+ * may both be NULL (keys and values only).  positions[i] < 0 marks a padding
+ * row: nothing of it is written.  slots[i] < 0: the token is not cached.  Slots
+ * must differ; one past the pool is skipped with KS_ERR_INVALID_ARG in status.
+ */
+KS_API ks_status ks_rope_append_bf16(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     int32_t n_tokens, int32_t n_q_heads,
+                                     const ks_page_pool* pool, const int32_t* positions,
+                                     const int32_t* slots, double rope_base, void* q_out,
+                                     int32_t* status, ks_stream_t stream);
+
+/*
+ * Causal grouped-query attention of a step's tokens over the paged cache:
+ *   out[i][h] = sum_j softmax_j(q[i][h] . K_j / sqrt(head_dim)) V_j
+ * over the keys j that token i at position p sees: j <= p, and with window > 0
+ * also j > p - window or j < n_sinks (a sliding window, and the first tokens
+ * that stay visible; n_sinks is ignored when window = 0).  K, V are kv head
+ * h / (n_q_heads / n_kv_heads) of the request's pages.  One token per request
+ * is a drafting step, a few a verification, many a prompt chunk.
+ * q, out: device bf16 [n_tokens][n_q_heads][head_dim] (must not overlap);
+ * block_table: device [B][max_blocks]; cu_new: device [B+1]; kv_len: device
+ * [B].  n_q_heads / n_kv_heads is at most 128.  max_new bounds every request's
+ * new tokens (it sizes the row tiles; the lengths themselves stay on the
+ * device, so a captured call follows them).
+ * A token that sees no key (kv_len shorter than the chunk) gets zeros; rows
+ * behind cu_new[B] are left as they are.  Pages without a visible key are not
+ * read (their entries may hold anything), nor does what a page holds at
+ * positions that no token of the request sees, NaN included, reach a result.
+ * Between tokens of one chunk the values must be finite: a key that a later
+ * token sees enters an earlier one's sum with weight zero.
+ * A page id outside the pool counts as a page of zeros and, like a request
+ * whose lengths break max_new, n_tokens or max_blocks (its excess is dropped),
+ * puts KS_ERR_INVALID_ARG in status.
+ * workspace: device, 256-byte aligned, ks_paged_attention_workspace_size()
+ * bytes, zero before its first use; every call leaves it fit for the next one
+ * (of any shape), so it needs no clearing again unless status reports
+ * KS_ERR_TIMEOUT.  Calls that overlap need a workspace each; one that does not
+ * start out zero is KS_ERR_WORKSPACE in status.
+ * Long key ranges are cut over the GPU's SMs and the pieces joined in a fixed
+ * order: the same call gives the same bits, but a row's last bits depend on the
+ * step's lengths.
+ */
+KS_API ks_status ks_paged_attention_workspace_size(size_t* bytes);
+KS_API ks_status ks_paged_attention_bf16(const void* q, const ks_page_pool* pool,
+                                         const int32_t* block_table, int32_t max_blocks,
+                                         const int32_t* cu_new, const int32_t* kv_len, int32_t B,
+                                         int32_t n_tokens, int32_t max_new, int32_t n_q_heads,
+                                         int32_t window, int32_t n_sinks, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         int32_t* status, ks_stream_t stream);
+
+/*
  * a2 / a3 -- one sublayer on a batch of E states (Eq. 7's "execute" branch).
  * Attention (item 2l): H + Wo . Attn(RoPE(Wq . RMSNorm(H))) with causal GQA
  * over the cache; MLP (item 2l+1): H + W_down (silu(W_gate x) * W_up x),

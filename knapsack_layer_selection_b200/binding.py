@@ -50,6 +50,12 @@ class CacheDesc(ctypes.Structure):
                 ("kv_mode", ctypes.c_int32)]
 
 
+class PagePool(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 KS_BUDGET_AT_MOST, KS_BUDGET_EXACT = 0, 1
 
 
@@ -80,7 +86,8 @@ EXPORTS = ["ks_version", "ks_last_error", "ks_status_string", "ks_quantize_weigh
            "ks_profile_start", "ks_profile_stop", "ks_reference_forward_noalloc",
            "ks_workspace_status", "ks_gemm_bf16", "ks_attention_bf16",
            "ks_check_bounded_wait", "ks_lemma_workspace_size", "ks_lemma_check", "ks_eval_set",
-           "ks_workspace_size_contexts", "ks_solve_contexts"]
+           "ks_workspace_size_contexts", "ks_solve_contexts", "ks_page_plan",
+           "ks_rope_append_bf16", "ks_paged_attention_workspace_size", "ks_paged_attention_bf16"]
 
 _lib = None
 
@@ -121,6 +128,13 @@ def load() -> ctypes.CDLL:
         "ks_eval_set": ([P, P, P, I32, P, P, P, P, P, P, SZ, P], ctypes.c_int),
         "ks_workspace_size_contexts": ([P, I32, P, I32, ctypes.POINTER(SZ)], ctypes.c_int),
         "ks_solve_contexts": ([P, P, I32, P, I32, P, P, P, P, P, SZ, P, P], ctypes.c_int),
+        "ks_page_plan": ([P, P, I32, P, I32, I32, I32, P, I32, I32, P, P, P, P, P, P, P],
+                         ctypes.c_int),
+        "ks_rope_append_bf16": ([P, I64, P, I64, P, I64, I32, I32, P, P, P, D, P, P, P],
+                                ctypes.c_int),
+        "ks_paged_attention_workspace_size": ([ctypes.POINTER(SZ)], ctypes.c_int),
+        "ks_paged_attention_bf16": ([P, P, P, I32, P, P, I32, I32, I32, I32, I32, I32, P, P, SZ, P,
+                                     P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -366,6 +380,144 @@ def attention_bf16(q: torch.Tensor, k_layer: torch.Tensor, v_layer: torch.Tensor
                                     _dev(v_layer, torch.bfloat16, "v"), rows, R, T, Hq, Hkv, hd,
                                     ctx, _dev(out, torch.bfloat16, "out"),
                                     _dev(status, torch.int32, "status"), _stream()))
+
+
+# ---------------------------------------------------------------- paged cache
+def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
+              block_table: torch.Tensor, page_size: int, n_pages: int, cu_new: torch.Tensor,
+              kv_len: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+              n_taken: torch.Tensor, status: Optional[torch.Tensor] = None) -> None:
+    """A step's layout from the requests' lengths (ks_page_plan), all int32:
+    ctx_len, new_len, kv_len [B], free_pages [n], block_table [B][max_blocks]
+    (updated in place), cu_new [B+1], positions, slots [max_tokens], n_taken [1]."""
+    B = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
+    _shape(ctx_len, (B,), "ctx_len")
+    _shape(new_len, (B,), "new_len")
+    _shape(kv_len, (B,), "kv_len")
+    _shape(cu_new, (B + 1,), "cu_new")
+    _shape(n_taken, (1,), "n_taken")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise KnapSpecError(f"block_table must be [{B}][max_blocks], got {tuple(block_table.shape)}")
+    n_free, cap = free_pages.numel(), positions.numel()
+    _shape(free_pages, (n_free,), "free_pages")
+    _shape(positions, (cap,), "positions")
+    _shape(slots, (cap,), "slots")
+    if status is not None and status.numel() < 1:
+        raise KnapSpecError("status must hold one int32")
+    i32 = torch.int32
+    _check(load().ks_page_plan(_dev(ctx_len, i32, "ctx_len"), _dev(new_len, i32, "new_len"), B,
+                               _dev(free_pages, i32, "free_pages"), n_free, n_pages, page_size,
+                               _dev(block_table, i32, "block_table"), block_table.shape[1], cap,
+                               _dev(cu_new, i32, "cu_new"), _dev(kv_len, i32, "kv_len"),
+                               _dev(positions, i32, "positions"), _dev(slots, i32, "slots"),
+                               _dev(n_taken, i32, "n_taken"), _dev(status, i32, "status"),
+                               _stream()))
+
+
+def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor) -> PagePool:
+    """One layer's pages [n_pages][page_size][Hkv][hd] of K and V."""
+    if k_pages.dim() != 4:
+        raise KnapSpecError("k_pages / v_pages must both be [n_pages][page_size][Hkv][hd]")
+    n_pages, page_size, Hkv, hd = k_pages.shape
+    _shape(v_pages, (n_pages, page_size, Hkv, hd), "v_pages")
+    return PagePool(_dev(k_pages, torch.bfloat16, "k_pages"), _dev(v_pages, torch.bfloat16, "v_pages"),
+                    n_pages, page_size, Hkv, hd)
+
+
+def _token_stride(t: torch.Tensor, shape: Sequence[int], name: str) -> int:
+    """Row stride of [tokens][heads][hd] rows whose heads lie side by side (a
+    slice of a fused projection's output will do)."""
+    _shape(t, shape, name)
+    n, H, hd = shape
+    if t.is_contiguous():
+        return H * hd
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != hd):
+        raise KnapSpecError(f"{name}: a token's heads must lie side by side, "
+                            f"got strides {tuple(t.stride())}")
+    return t.stride(0) if n > 1 else H * hd
+
+
+def _strided_dev(t: Optional[torch.Tensor], name: str) -> Optional[int]:
+    """_dev for bf16 rows that _token_stride has accepted."""
+    if t is None:
+        return None
+    _dev(t[:0], torch.bfloat16, name)          # device and dtype
+    return t.data_ptr()
+
+
+def rope_append_bf16(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                     positions: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
+                     v_pages: torch.Tensor, rope_base: float, q_out: Optional[torch.Tensor],
+                     status: Optional[torch.Tensor] = None) -> None:
+    """Rotate a step's queries into q_out and its keys into their pages, beside
+    its values (ks_rope_append_bf16): q, q_out [n][Hq][hd] (or both None),
+    k, v [n][Hkv][hd], positions, slots [>= n] int32."""
+    if k.dim() != 3:
+        raise KnapSpecError(f"k must be [n][Hkv][hd], got {tuple(k.shape)}")
+    n, Hkv, hd = k.shape
+    _shape(k_pages, tuple(k_pages.shape[:2]) + (Hkv, hd), "k_pages")
+    for t, name in ((positions, "positions"), (slots, "slots")):
+        _rows(t, n, (), name)
+    if (q is None) != (q_out is None):
+        raise KnapSpecError("q and q_out go together")
+    Hq, qs = 1, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise KnapSpecError(f"q must be [n][Hq][hd], got {tuple(q.shape)}")
+        Hq = q.shape[1]
+        qs = _token_stride(q, (n, Hq, hd), "q")
+        _shape(q_out, (n, Hq, hd), "q_out")
+    ks = _token_stride(k, (n, Hkv, hd), "k")
+    vs = _token_stride(v, (n, Hkv, hd), "v")
+    _shape(v_pages, tuple(k_pages.shape), "v_pages")
+    if status is not None and status.numel() < 1:
+        raise KnapSpecError("status must hold one int32")
+    pool = _pool(k_pages, v_pages)
+    _check(load().ks_rope_append_bf16(_strided_dev(q, "q"), qs, _strided_dev(k, "k"), ks,
+                                      _strided_dev(v, "v"), vs, n, Hq, ctypes.byref(pool),
+                                      _dev(positions, torch.int32, "positions"),
+                                      _dev(slots, torch.int32, "slots"), rope_base,
+                                      _dev(q_out, torch.bfloat16, "q_out"),
+                                      _dev(status, torch.int32, "status"), _stream()))
+
+
+def paged_attention_workspace_size() -> int:
+    out = ctypes.c_size_t()
+    _check(load().ks_paged_attention_workspace_size(ctypes.byref(out)))
+    return out.value
+
+
+def paged_attention_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for paged_attention_bf16: zero, as its first use wants it."""
+    return torch.zeros(paged_attention_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def paged_attention_bf16(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         block_table: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor,
+                         max_new: int, out: torch.Tensor, ws: torch.Tensor, window: int = 0,
+                         sinks: int = 0, status: Optional[torch.Tensor] = None) -> None:
+    """Causal GQA attention of a step's tokens over the paged cache
+    (ks_paged_attention_bf16): q, out [n][Hq][hd] bf16, k_pages, v_pages
+    [n_pages][page_size][Hkv][hd] bf16, block_table [B][max_blocks], cu_new
+    [B+1], kv_len [B] int32; ws from paged_attention_workspace()."""
+    if q.dim() != 3:
+        raise KnapSpecError(f"q must be [n][Hq][hd], got {tuple(q.shape)}")
+    n, Hq, hd = q.shape
+    _shape(out, (n, Hq, hd), "out")
+    _shape(k_pages, tuple(k_pages.shape[:3]) + (hd,), "k_pages")
+    if block_table.dim() != 2:
+        raise KnapSpecError(f"block_table must be [B][max_blocks], got {tuple(block_table.shape)}")
+    B, max_blocks = block_table.shape
+    _shape(cu_new, (B + 1,), "cu_new")
+    _shape(kv_len, (B,), "kv_len")
+    if status is not None and status.numel() < 1:
+        raise KnapSpecError("status must hold one int32")
+    pool = _pool(k_pages, v_pages)
+    _check(load().ks_paged_attention_bf16(
+        _dev(q, torch.bfloat16, "q"), ctypes.byref(pool), _dev(block_table, torch.int32, "block_table"),
+        max_blocks, _dev(cu_new, torch.int32, "cu_new"), _dev(kv_len, torch.int32, "kv_len"), B, n,
+        max_new, Hq, window, sinks, _dev(out, torch.bfloat16, "out"), _dev(ws, name="workspace"),
+        ws.numel() * ws.element_size(), _dev(status, torch.int32, "status"), _stream()))
 
 
 def check_bounded_wait(limit_us: int, status: torch.Tensor,

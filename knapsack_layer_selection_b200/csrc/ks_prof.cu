@@ -49,7 +49,8 @@ const char* kernel_kind_name(int k) {
                                         "gemm_gateup_swiglu", "gemm_down_residual", "rope",
                                         "swiglu", "attention", "select_bp", "reconstruct",
                                         "tpt_argmax", "init_states", "rope_table", "dedup",
-                                        "gather", "dedup_verify", "gemm_kv_window"};
+                                        "gather", "dedup_verify", "gemm_kv_window", "page_plan",
+                                        "rope_append", "paged_attention"};
   return (k >= 0 && k < KK_COUNT) ? names[k] : "?";
 }
 

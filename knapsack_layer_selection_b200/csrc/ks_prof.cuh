@@ -25,6 +25,9 @@ enum KernelKind {
   KK_GATHER,
   KK_DEDUP_VERIFY,
   KK_GEMM_KV,
+  KK_PAGE_PLAN,
+  KK_ROPE_APPEND,
+  KK_PAGED_ATTN,
   KK_COUNT
 };
 
