@@ -1,13 +1,18 @@
 // Attention of a chunk of new tokens over the paged cache: the plain form, one
 // warp per (token, query head) that walks its visible keys with a running
 // maximum and sum.
-#include "ks_paged.cuh"
+#include <math.h>
+
+#include <algorithm>
+
+#include "ks_paged_sched.cuh"
+#include "ks_tc.cuh"
 
 namespace ks {
 
 namespace {
 
-struct Params {
+struct Simple {
   const __nv_bfloat16 *q, *k, *v;
   __nv_bfloat16* out;
   const int32_t *table, *cu, *kv_len;
@@ -17,7 +22,7 @@ struct Params {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const Params p) {
+__global__ void __launch_bounds__(128) paged_attn_kernel(const Simple p) {
   constexpr int E = HD / 32;
   const int i = blockIdx.x, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
@@ -67,18 +72,46 @@ __global__ void __launch_bounds__(128) paged_attn_kernel(const Params p) {
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes() { return 4096; }
+size_t paged_attention_workspace_bytes() { return paged::kWorkspaceBytes; }
 
 ks_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t st) {
-  const int hd = a.pool->head_dim;
-  const Params p{(const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.pool->k_pages,
-                 (const __nv_bfloat16*)a.pool->v_pages, (__nv_bfloat16*)a.out, a.block_table,
+  const ks_page_pool& pool = *a.pool;
+  paged::Params p{};
+  p.table = a.block_table;
+  p.cu = a.cu_new;
+  p.kv_len = a.kv_len;
+  p.out = (__nv_bfloat16*)a.out;
+  p.ws = (unsigned char*)a.workspace;
+  p.status = a.status;
+  p.B = a.B;
+  p.n_tokens = a.n_tokens;
+  p.max_new = std::min(a.max_new, a.n_tokens);
+  p.max_blocks = a.max_blocks;
+  p.page_size = pool.page_size;
+  p.cap = a.max_blocks * pool.page_size;
+  p.Hq = a.Hq;
+  p.Hkv = pool.n_kv_heads;
+  p.grp = a.Hq / pool.n_kv_heads;
+  p.n_pages = pool.n_pages;
+  p.n_slots = pool.n_pages * pool.page_size;
+  p.box = std::min(paged::kBlock, pool.page_size & -pool.page_size);
+  p.window = a.window < p.cap ? a.window : 0;   // a window that no position outruns hides nothing
+  p.sinks = a.n_sinks;
+  p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)pool.head_dim));
+  if ((long long)p.grp * p.max_new <= 128) {
+    p.tile_tokens = p.max_new;
+    const long long most = (long long)p.B * p.Hkv * std::max(1, ceil_div(p.cap, paged::kBlock));
+    const int grid = (int)std::min<long long>(std::min(sm_count(), paged::kMaxCtas), most);
+    return launch_paged_decode(a, p, grid, st);
+  }
+  const Simple s{(const __nv_bfloat16*)a.q, (const __nv_bfloat16*)pool.k_pages,
+                 (const __nv_bfloat16*)pool.v_pages, (__nv_bfloat16*)a.out, a.block_table,
                  a.cu_new, a.kv_len, a.status, a.max_blocks, a.B, a.n_tokens, a.max_new, a.Hq,
-                 a.pool->n_kv_heads, a.pool->page_size, a.pool->n_pages, a.window, a.n_sinks,
-                 1.0f / sqrtf((float)hd)};
+                 pool.n_kv_heads, pool.page_size, pool.n_pages, a.window, a.n_sinks,
+                 1.0f / sqrtf((float)pool.head_dim)};
   const dim3 grid(a.n_tokens, (a.Hq + 3) / 4);
-  if (hd == 128) paged_attn_kernel<128><<<grid, 128, 0, st>>>(p);
-  else paged_attn_kernel<64><<<grid, 128, 0, st>>>(p);
+  if (pool.head_dim == 128) paged_attn_kernel<128><<<grid, 128, 0, st>>>(s);
+  else paged_attn_kernel<64><<<grid, 128, 0, st>>>(s);
   KS_LAUNCH_CHECK();
   return KS_OK;
 }

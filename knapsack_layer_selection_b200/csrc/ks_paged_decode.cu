@@ -1,0 +1,627 @@
+// Attention over the paged cache for up to 128 query rows per request and kv
+// head: one token each (a drafting step), a few (a verification), a short chunk
+// (sm_100a, tcgen05 + TMEM + TMA).
+//
+// Every key and value is read once, and a row of them meets few queries, so the
+// keys' traffic bounds it.  The products are turned round so that the keys fill
+// the tensor core's 128 rows and the queries are its (16 .. 128) columns:
+//   S^T = K Q^T      A = K block [128 keys][hd],       B = Q [rows][hd]
+//   O^T += V^T P^T   A = V block read MN-major [hd][128], B = P [rows][128 keys]
+// A thread of the softmax is then a key, and its work is one exponential per
+// query row: with 4 rows a block costs a thread 4 to 8 exponentials, where query
+// rows on the lanes would leave 28 of 32 lanes idle behind 128 each.
+//
+// One persistent CTA per SM takes an equal share of the step's key blocks
+// (ks_paged_sched.cuh); 384 threads:
+//   warp 0    -- TMA: per piece its Q tile (two buffers), and one ring of 128-key
+//                tiles in the order K_0, K_1, V_0, K_2, V_1, ...; each lane loads
+//                the box of one page (the largest power of two of keys, up to
+//                128, that divides the page) of one 64-column panel;
+//   warp 1    -- S_{i+1}, then P.V_i, for the whole share: across pieces too, so
+//                a short piece's tail hides the next one's first products;
+//   warp 2    -- TMEM owner;
+//   warp 3    -- walks the share and publishes its pieces;
+//   warps 4-11 -- two softmax groups, each half of the query rows (TMEM columns),
+//                thread = key.  P goes to shared memory (two buffers).
+// The softmax reference of a row is kept until a score exceeds it by 2^8, so a
+// block needs no maximum: each thread only compares, one vote of the group finds
+// the rare block that moves a reference (and always a piece's first), and only
+// then are maxima taken over the keys and O rescaled.  Row sums stay with the
+// keys' threads in fp32 and are added up once per piece; P is rounded to bf16 for
+// the tensor core, O is fp32.
+#include <algorithm>
+
+#include "ks_paged_sched.cuh"
+#include "ks_tc.cuh"
+
+namespace ks {
+
+using namespace paged;
+
+namespace {
+
+constexpr int kMaxRing = 12;
+constexpr int kSmemLimit = 232448;
+constexpr int kSmemFloor = 118784;             // one CTA holds an SM and its 512 TMEM columns
+
+struct Tail {
+  SchedSmem sched;
+  uint64_t full[kMaxRing], empty[kMaxRing];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];   // by block parity
+  uint64_t o_free;                                        // one phase per piece
+  uint64_t gsync[2], esync, drain;                        // meetings of a group's / all softmax warps
+  uint32_t tmem_base;
+  int abort, last;
+  alignas(16) int vote[2][2][4];                                 // [group][block parity][warp]
+  alignas(16) float nref[128], alpha[128];                // -reference and rescale factor by row
+  float wmax[4][128], lsum[4][128];                       // by warp and row
+};
+constexpr int kTailBytes = (int)((sizeof(Tail) + 255) / 256 * 256);
+
+template <int HD>
+constexpr int slot_bytes() { return HD / 64 * kBlock * 128; }
+
+// 8 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+// Ties registers filled by tcgen05.ld to the point after its wait.
+__device__ __forceinline__ void reg_fence8(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]));
+}
+
+// Largest of the warp's values; floats compare like integers once the negative
+// ones' lower bits are flipped.
+__device__ __forceinline__ float warp_max(float x) {
+  int i = __float_as_int(x);
+  i ^= (i >> 31) & 0x7fffffff;
+  i = __reduce_max_sync(0xffffffffu, i);
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// Sums of 8 values over the warp's lanes: lane l returns the sum of v[l / 4].
+// Each exchange halves the values a lane still carries, so 8 sums take 9 shuffles.
+__device__ __forceinline__ float warp_sum8(const float* v, int lane) {
+  float a[4], b[2], c;
+  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a[i] = (h16 ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, h16 ? v[i] : v[i + 4], 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    b[i] = (h8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, h8 ? a[i] : a[i + 2], 8);
+  c = (h4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, h4 ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+// CPG: most query rows that one softmax group handles (half of a tile's).
+template <int HD, int CPG>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  constexpr int PANELS = HD / 64, SLOT = slot_bytes<HD>(), NCH = CPG / 8;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  // the 128-byte-swizzled tiles need a 1024-aligned base; refuse rather than realign
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) raise_status(p.status, KS_ERR_INTERNAL);
+    return;
+  }
+  const int N = p.q_rows, row_panel = N * 128;           // a 64-column panel of N rows
+  const int q_tile = PANELS * row_panel, p_tile = 2 * row_panel;
+  const int off_q = p.n_slots_ring * SLOT, off_p = off_q + p.q_bufs * q_tile;
+  Tail* tail = reinterpret_cast<Tail*>(smem + off_p + 2 * p_tile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &tail->abort;
+  const uint32_t sbase = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.n_slots_ring; ++s) {
+      mbar_init(smem_u32(&tail->full[s]), 1);
+      mbar_init(smem_u32(&tail->empty[s]), 1);
+    }
+    for (int s = 0; s < kSegRing; ++s) {
+      mbar_init(smem_u32(&tail->sched.full[s]), 1);
+      mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // TMA, S, P.V and 8 softmax warps
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&tail->q_full[b]), 1);
+      mbar_init(smem_u32(&tail->q_empty[b]), 1);
+      mbar_init(smem_u32(&tail->s_full[b]), 1);
+      mbar_init(smem_u32(&tail->s_free[b]), 8);
+      mbar_init(smem_u32(&tail->p_full[b]), 8);
+      mbar_init(smem_u32(&tail->pv_done[b]), 1);
+      mbar_init(smem_u32(&tail->gsync[b]), 4);
+    }
+    mbar_init(smem_u32(&tail->o_free), 8);
+    mbar_init(smem_u32(&tail->esync), 8);
+    mbar_init(smem_u32(&tail->drain), 1);
+    tail->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&tail->tmem_base), 512);
+    tmem_relinquish();
+  }
+  // rows of a Q tile that no load writes (the tile's rows rounded up to 16)
+  const int box_rows = p.grp * p.tile_tokens;
+  for (int e = threadIdx.x; e < p.q_bufs * PANELS * (N - box_rows) * 8; e += kThreads) {
+    const int pn = e / ((N - box_rows) * 8), o = e - pn * ((N - box_rows) * 8);
+    reinterpret_cast<uint4*>(smem + off_q + pn * row_panel + box_rows * 128)[o] =
+        make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  locate(p, tail->sched);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tail->tmem_base;
+  constexpr uint32_t kS = 0, kO = 256;         // TMEM columns: S[b] at 128 b, then O
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    SegReader rd;
+    Seg s;
+    int slot = 0, n_loads = 0, prev_row = 0, prev_g = 0, n_seg = 0;
+    uint32_t phase = 1;
+    bool ok = true, have_prev = false;
+    const int nbox = kBlock / p.box;
+    const bool mine = (lane & 15) < nbox && (lane >> 4) < PANELS;
+    const uint32_t box_off = (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
+    if (lane == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    auto load = [&](const CUtensorMap* tm, int row, int g) -> bool {
+      if (!KS_PAGED_WAIT(tail->empty[slot], phase)) return false;
+      const uint32_t fb = smem_u32(&tail->full[slot]);
+      if (lane == 0) mbar_arrive_expect_tx(fb, SLOT);
+      __syncwarp();
+      if (mine) tma_load_2d(sbase + slot * SLOT + box_off, tm, g * HD + (lane >> 4) * 64, row, fb);
+      ++n_loads;
+      if (++slot == p.n_slots_ring) {
+        slot = 0;
+        phase ^= 1;
+      }
+      return true;
+    };
+    while (ok) {
+      if (!rd.take(p, tail->sched, abort, s)) break;
+      if (s.nb == 0) {
+        if (have_prev) load(&tmV, prev_row, prev_g);
+        break;
+      }
+      BoxRow next;
+      next.fetch(p, s, s.key_block(0), lane);
+      const int qb = n_seg % p.q_bufs;
+      if (!KS_PAGED_WAIT(tail->q_empty[qb], ((n_seg / p.q_bufs) & 1) ^ 1)) break;
+      if (lane == 0) {
+        const uint32_t qf = smem_u32(&tail->q_full[qb]);
+        mbar_arrive_expect_tx(qf, PANELS * box_rows * 128);
+        for (int pn = 0; pn < PANELS; ++pn)
+          tma_load_3d(sbase + off_q + qb * q_tile + pn * row_panel, &tmQ, pn * 64, s.g * p.grp,
+                      s.row0, qf);
+      }
+      ++n_seg;
+      for (int i = 0; ok && i < s.nb; ++i) {
+        const BoxRow cur = next;
+        if (i + 1 < s.nb) next.fetch(p, s, s.key_block(i + 1), lane);
+        const int row = cur.slot(p);
+        ok = load(&tmK, row, s.g);
+        if (ok && have_prev) ok = load(&tmV, prev_row, prev_g);
+        prev_row = row;
+        prev_g = s.g;
+        have_prev = true;
+      }
+    }
+    // drain the copies still in flight before leaving
+    if (lane == 0) {
+      for (int n = n_seg > p.q_bufs ? n_seg - p.q_bufs : 0; n < n_seg; ++n)
+        mbar_wait_drain(smem_u32(&tail->q_full[n % p.q_bufs]), (n / p.q_bufs) & 1, p.status);
+      for (int n = n_loads > p.n_slots_ring ? n_loads - p.n_slots_ring : 0; n < n_loads; ++n)
+        mbar_wait_drain(smem_u32(&tail->full[n % p.n_slots_ring]),
+                        (uint32_t)(n / p.n_slots_ring) & 1, p.status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    SegReader rs, rp;                          // the pieces of S, and those of P.V behind it
+    Seg ss, sp;
+    ss.nb = sp.nb = 0;
+    int si = 0, pi = 0, slot = 0, s_segs = 0, qb = 0;
+    uint32_t phase = 0, i = 0, j = 0, p_segs = 0;
+    bool s_end = false;
+    const uint32_t idesc_s = idesc_bf16_f32(128, N);
+    const uint32_t idesc_o = idesc_bf16_f32(128, N) | (1u << 15);   // A (V) MN-major
+    const uint64_t dk0 = desc_kmajor_sw128(sbase), dq0 = desc_kmajor_sw128(sbase + off_q);
+    const uint64_t dp0 = desc_kmajor_sw128(sbase + off_p);
+    // head_dim 64: rows 64 .. 127 of the product repeat V's columns some keys further on; nobody
+    // reads them
+    const uint64_t dv0 = desc_mnmajor_sw128(sbase, PANELS == 2 ? kBlock * 128 : 1024);
+    const uint32_t rp16 = row_panel >> 4;
+    auto step_ring = [&] {
+      if (++slot == p.n_slots_ring) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    // S_i = K_i Q^T into S buffer i % 2, free once the softmax has copied S_{i-2}
+    auto issue_s = [&]() -> bool {
+      if (s_end) return true;
+      if (si == ss.nb) {
+        if (!rs.take(p, tail->sched, abort, ss)) return false;
+        si = 0;
+        if (ss.nb == 0) {
+          s_end = true;
+          return true;
+        }
+        qb = s_segs % p.q_bufs;
+        if (!KS_PAGED_WAIT(tail->q_full[qb], (s_segs / p.q_bufs) & 1)) return false;
+        ++s_segs;
+      }
+      const uint32_t b = i & 1;
+      if (i >= 2 && !KS_PAGED_WAIT(tail->s_free[b], ((i - 2) >> 1) & 1)) return false;
+      if (!KS_PAGED_WAIT(tail->full[slot], phase)) return false;
+      tc_fence_after();
+      ++si;
+      if (lane == 0) {
+        const uint64_t dk = dk0 + (uint64_t)((slot * SLOT) >> 4);
+        const uint64_t dq = dq0 + (uint64_t)((qb * q_tile) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          mma_bf16(tmem + kS + b * 128, dk + (uint64_t)((kk / 4) * ((kBlock * 128) >> 4) + 2 * (kk % 4)),
+                   dq + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc_s, kk > 0);
+        mma_commit(smem_u32(&tail->s_full[b]));
+        mma_commit(smem_u32(&tail->empty[slot]));
+        if (si == ss.nb) mma_commit(smem_u32(&tail->q_empty[qb]));
+      }
+      __syncwarp();
+      step_ring();
+      ++i;
+      return true;
+    };
+    bool ok = issue_s();
+    while (ok && (ok = issue_s())) {
+      // O^T += V_j^T P_j once the softmax has written P_j
+      if (pi == sp.nb) {
+        if (!rp.take(p, tail->sched, abort, sp)) break;
+        if (sp.nb == 0) break;
+        pi = 0;
+        if (p_segs > 0 && !KS_PAGED_WAIT(tail->o_free, (p_segs - 1) & 1)) break;
+        ++p_segs;
+      }
+      const uint32_t b = j & 1;
+      if (!KS_PAGED_WAIT(tail->full[slot], phase)) break;
+      const int kb = sp.key_block(pi);
+      if (sp.ragged(kb)) zero_unseen<PANELS>(sp, kb, smem + slot * SLOT, lane);
+      if (!KS_PAGED_WAIT(tail->p_full[b], (j >> 1) & 1)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t dv = dv0 + (uint64_t)((slot * SLOT) >> 4);
+        const uint64_t dp = dp0 + (uint64_t)((b * p_tile) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBlock / 16; ++kk)
+          mma_bf16(tmem + kO, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
+                   dp + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc_o, pi > 0 || kk > 0);
+        mma_commit(smem_u32(&tail->pv_done[b]));
+        mma_commit(smem_u32(&tail->empty[slot]));
+      }
+      __syncwarp();
+      step_ring();
+      ++pi;
+      ++j;
+    }
+    if (lane == 0) {
+      mma_commit(smem_u32(&tail->drain));
+      mbar_wait_drain(smem_u32(&tail->drain), 0, p.status);
+    }
+  } else if (warp == 3) {
+    schedule(p, tail->sched, abort);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int G = (warp - 4) >> 2, q4 = warp & 3;
+    const int key = q4 * 32 + lane;            // key of the block = TMEM lane
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const float sl2 = p.scale_log2;
+    // byte of this key in a row of P: 64-key panel, and the swizzled 16-byte chunk of row e % 8
+    const uint32_t p_key = (key >> 6) * row_panel + (key & 7) * 2;
+    const uint32_t p_chunk = (key & 63) >> 3;
+    SegReader rd;
+    Seg s;
+    uint32_t j = 0, syncs = 0, esyncs = 0;
+    bool ok = true;
+    auto meet = [&]() -> bool {                // the group's four warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->gsync[G]));
+      return KS_PAGED_WAIT(tail->gsync[G], syncs++ & 1);
+    };
+    auto meet_all = [&]() -> bool {            // all eight
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->esync));
+      return KS_PAGED_WAIT(tail->esync, esyncs++ & 1);
+    };
+    // PV_q commits to pv_done[q % 2]; whoever waits for it has waited for PV_{q-2} before, and
+    // PV_{q+2} needs a P that this warp has not written, so the parity is unambiguous
+    auto wait_pv = [&](uint32_t q) -> bool {
+      if (!KS_PAGED_WAIT(tail->pv_done[q & 1], (q >> 1) & 1)) return false;
+      tc_fence_after();
+      return true;
+    };
+    while (ok) {
+      if (!rd.take(p, tail->sched, abort, s) || s.nb == 0) break;
+      const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
+      const int r0 = G ? half * 8 : 0;         // this group's first row
+      const int nch = G ? chunks - half : half;
+      float l[CPG];
+#pragma unroll
+      for (int c = 0; c < CPG; ++c) l[c] = 0.f;
+      for (int i = 0; ok && i < s.nb; ++i, ++j) {
+        const uint32_t b = j & 1;
+        if (!KS_PAGED_WAIT(tail->s_full[b], (j >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sc[CPG];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          if (c < nch) tmem_ld8(tmem + lanes + kS + b * 128 + r0 + c * 8, &sc[c * 8]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) reg_fence8(&sc[c * 8]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[b]));   // S_{j+2} may be computed now
+        if (nch > 0) {
+          const int kb = s.key_block(i);
+          if (s.masked(p, kb)) {
+            // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
+            // on, and while the key is in its window up to row (k - p_first + window) grp
+            const int k = kb * kBlock + key;
+            const long long d = (long long)k - s.p_first;
+            const int from = (int)(d < 0 ? 0 : d > 128 ? 128 : d) * p.grp;
+            int to = 1 << 20;
+            if (p.window > 0 && k >= p.sinks) {
+              const long long e = d + p.window;
+              to = (int)(e < 0 ? 0 : e > 128 ? 128 : e) * p.grp;
+            }
+#pragma unroll
+            for (int c = 0; c < CPG; ++c)
+              if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;
+          }
+          // has a score outgrown its row's reference?
+          bool grow = i == 0;
+          if (i > 0) {
+            bool any = false;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+              if (c < nch) {
+                const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+                const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+                const float* x = &sc[c * 8];
+                const float m0 = fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
+                const float m1 = fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
+                any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
+              }
+            any = __any_sync(0xffffffffu, any);
+            if (lane == 0) tail->vote[G][b][q4] = any;
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+            const int4 v = *reinterpret_cast<const int4*>(tail->vote[G][b]);
+            grow = v.x | v.y | v.z | v.w;
+          }
+          if (grow) {
+            // maxima over the keys, and the rows' new references
+#pragma unroll
+            for (int c0 = 0; c0 < CPG; c0 += 32) {
+              float m = 0.f;
+#pragma unroll
+              for (int c = c0; c < c0 + 32 && c < CPG; ++c)
+                if (c < nch * 8) {
+                  const float w = warp_max(sc[c]);
+                  if (lane == c - c0) m = w;
+                }
+              if (c0 + lane < nch * 8) tail->wmax[q4][r0 + c0 + lane] = m;
+            }
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+            if (key < nch * 8) {
+              const int r = r0 + key;
+              const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
+                                           fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
+              const float old = i == 0 ? kNoRef : -tail->nref[r];
+              const bool up = mx - old > kStale;
+              tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
+              tail->nref[r] = up ? -mx : -old;
+            }
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+            if (i > 0) {
+              // sums and O hold the blocks before relative to the old references
+              if (!wait_pv(j - 1)) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int c = 0; c < NCH; ++c)
+                if (c < nch) {
+                  float v[8];
+                  const uint32_t to = tmem + lanes + kO + r0 + c * 8;
+                  tmem_ld8(to, v);
+                  tmem_wait_ld();
+                  reg_fence8(v);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const float a = tail->alpha[r0 + c * 8 + e];
+                    v[e] *= a;
+                    l[c * 8 + e] *= a;
+                  }
+                  tmem_st8(to, v);
+                }
+              tmem_wait_st();
+            }
+          }
+          // the P buffer was last read by PV_{j-2}
+          if (j >= 2 && !wait_pv(j - 2)) {
+            ok = false;
+            break;
+          }
+          unsigned char* pt = smem + off_p + b * p_tile + p_key + r0 * 128;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            if (c < nch) {
+              const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+              const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+              const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float w = ex2(fmaf(sc[c * 8 + e], sl2, n[e]));
+                l[c * 8 + e] += w;
+                *reinterpret_cast<__nv_bfloat16*>(pt + (c * 8 + e) * 128 + ((p_chunk ^ e) << 4)) =
+                    __float2bfloat16_rn(w);
+              }
+            }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else if (j >= 2 && !wait_pv(j - 2)) {   // keep in step
+          ok = false;
+          break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail->p_full[b]));
+      }
+      if (!ok) break;
+      // -------------------------------------------------------- a piece is done
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        if (c < nch) {
+          const float w = warp_sum8(&l[c * 8], lane);
+          if ((lane & 3) == 0) tail->lsum[q4][r0 + c * 8 + (lane >> 2)] = w;
+        }
+      if (!wait_pv(j - 1) || !meet()) break;
+      const bool cut = s.nb < s.blocks;
+      float o[CPG];
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        if (c < nch) tmem_ld8(tmem + lanes + kO + r0 + c * 8, &o[c * 8]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) reg_fence8(&o[c * 8]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->o_free));
+      if (!cut) {
+        int t = r0 / p.grp, hh = r0 - t * p.grp;
+        if (key < HD) {
+          __nv_bfloat16* dst = p.out + ((long long)(s.row0 + t) * p.Hq + s.g * p.grp + hh) * HD + key;
+          const long long next = (long long)(p.Hq - p.grp + 1) * HD;
+#pragma unroll
+          for (int c = 0; c < CPG; ++c)
+            if (c < nch * 8 && r0 + c < rows) {
+              const int r = r0 + c;
+              const float sum = (tail->lsum[0][r] + tail->lsum[1][r]) + (tail->lsum[2][r] + tail->lsum[3][r]);
+              *dst = __float2bfloat16_rn(sum > 0.f ? o[c] / sum : 0.f);
+              if (++hh == p.grp) {
+                hh = 0;
+                dst += next;
+              } else {
+                dst += HD;
+              }
+            }
+        }
+      } else {
+        unsigned char* pc = own_piece(p, s);
+        if (key < HD) {
+          float* dst = reinterpret_cast<float*>(pc + kPieceStats) + r0 * HD + key;
+#pragma unroll
+          for (int c = 0; c < CPG; ++c)
+            if (c < nch * 8 && r0 + c < rows) __stcg(dst + c * HD, o[c]);
+        }
+        if (key < nch * 8) {
+          const int r = r0 + key;
+          __stcg(reinterpret_cast<float2*>(pc) + r,
+                 make_float2(-tail->nref[r], (tail->lsum[0][r] + tail->lsum[1][r]) +
+                                                 (tail->lsum[2][r] + tail->lsum[3][r])));
+        }
+        __threadfence();
+        if (!meet_all()) break;
+        if (warp == 4 && lane == 0) tail->last = arrive_piece(p, s);
+        if (!meet_all()) break;
+        if (tail->last) {
+          __threadfence();
+          join_pieces<HD>(p, s, warp - 4, 8, lane);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD, int CPG>
+ks_status launch(Params p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                 int grid, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr{0};
+  auto k = paged_decode_kernel<HD, CPG>;
+  KS_TRY(once_per_device(attr, [&]() -> ks_status {
+    KS_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
+    return KS_OK;
+  }));
+  // a second Q buffer lets a piece's first product follow the last one's at once; above 64 rows its
+  // room is worth more as a fifth ring slot
+  p.q_bufs = p.q_rows <= 64 ? 2 : 1;
+  const int tiles = (p.q_bufs * (HD / 64) + 4) * p.q_rows * 128 + kTailBytes;   // Q, P and the rest
+  p.n_slots_ring = std::min(kMaxRing, (kSmemLimit - tiles) / slot_bytes<HD>());
+  const int smem = std::max(kSmemFloor, p.n_slots_ring * slot_bytes<HD>() + tiles);
+  k<<<grid, kThreads, smem, st>>>(tq, tk, tv, p);
+  KS_LAUNCH_CHECK();
+  return KS_OK;
+}
+
+template <int HD>
+ks_status launch_hd(const Params& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                    const CUtensorMap& tv, int grid, cudaStream_t st) {
+  const int rows = p.grp * p.tile_tokens;
+  if (rows <= 16) return launch<HD, 8>(p, tq, tk, tv, grid, st);
+  if (rows <= 32) return launch<HD, 16>(p, tq, tk, tv, grid, st);
+  if (rows <= 64) return launch<HD, 32>(p, tq, tk, tv, grid, st);
+  return launch<HD, 64>(p, tq, tk, tv, grid, st);
+}
+
+}  // namespace
+
+ks_status launch_paged_decode(const PagedAttnArgs& a, Params p, int grid, cudaStream_t st) {
+  const int hd = a.pool->head_dim;
+  p.q_rows = (p.grp * p.tile_tokens + 15) / 16 * 16;
+  const long long kvd = (long long)p.Hkv * hd;
+  CUtensorMap tq, tk, tv;
+  KS_TRY(make_tmap_heads(&tq, a.q, a.n_tokens, a.Hq, hd, p.grp, p.tile_tokens));
+  KS_TRY(make_tmap_2d(&tk, a.pool->k_pages, p.n_slots, kvd, kvd, 64, p.box));
+  KS_TRY(make_tmap_2d(&tv, a.pool->v_pages, p.n_slots, kvd, kvd, 64, p.box));
+  return hd == 128 ? launch_hd<128>(p, tq, tk, tv, grid, st) : launch_hd<64>(p, tq, tk, tv, grid, st);
+}
+
+}  // namespace ks

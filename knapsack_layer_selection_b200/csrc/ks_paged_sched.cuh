@@ -1,0 +1,475 @@
+// What the two paged-attention kernels share on the device: how a step's
+// requests become work, how a CTA walks its share, and how pieces are joined.
+//
+// Work is counted in key blocks (128 positions).  A unit is one tile of query
+// rows (whole tokens x the query heads of one kv head) with the key blocks that
+// its tokens see; units are ordered by request, kv head, tile, and their blocks
+// concatenated.  CTA c takes the c-th of G equal shares of that sequence, so
+// every SM gets the same number of blocks whatever the lengths; a unit that
+// crosses a border is cut into pieces there, at most two per CTA.  The lengths
+// are on the device: every CTA adds the requests' block counts up itself (they
+// come from L2) and finds its first block, which costs about as much as reading
+// them once and saves a launch.
+//
+// A piece leaves its unnormalised output, reference and row sum in the
+// workspace; the last CTA of a unit to arrive joins the pieces in their order,
+// so the result does not depend on who arrives last.
+#pragma once
+
+#include "ks_paged.cuh"
+#include "ks_sm100.cuh"
+
+namespace ks {
+namespace paged {
+
+using namespace sm100;
+
+constexpr int kBlock = 128;                  // keys per block
+constexpr int kMaxCtas = 148;                // one CTA per SM of a B200
+constexpr int kThreads = 384;                // both kernels: 12 warps
+constexpr int kWarps = kThreads / 32;
+constexpr float kNoRef = -1e30f;             // reference of a row that has seen no key
+constexpr float kStale = 8.0f;               // a new reference once the maximum grows by > 2^8
+
+// Workspace: one arrival counter per CTA (of the unit whose first piece it
+// holds), then two pieces per CTA: reference and sum of 128 rows, and the rows.
+constexpr size_t kCounterBytes = 1024;
+constexpr size_t kPieceStats = 128 * sizeof(float2);
+constexpr size_t kPieceBytes = kPieceStats + 128 * 128 * sizeof(float);
+constexpr size_t kWorkspaceBytes = kCounterBytes + 2 * kMaxCtas * kPieceBytes;
+static_assert(kMaxCtas * sizeof(int) <= kCounterBytes, "counters");
+
+struct Params {
+  const int32_t *table, *cu, *kv_len;
+  __nv_bfloat16* out;
+  unsigned char* ws;
+  int32_t* status;
+  int B, n_tokens, max_new, max_blocks, cap;   // cap = max_blocks * page_size positions a row
+  int Hq, Hkv, grp, page_size, n_pages, n_slots, box;   // box: keys per TMA box
+  int window, sinks;
+  int tile_tokens;                             // tokens per query tile
+  int q_rows;                                  // decode kernel: rows of a Q / P tile (N)
+  int n_slots_ring, q_bufs;                    // decode kernel: ring slots, Q buffers
+  float scale_log2;
+};
+
+// A request's rows after every clamp that keeps broken lengths inside the
+// buffers; pos0 (of its first token) is negative where kv_len is shorter than
+// the chunk.
+struct Req {
+  int row0, n, pos0;
+};
+
+__device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
+  const long long c0 = p.cu[b], c1 = p.cu[b + 1];
+  const int kv_in = p.kv_len[b];
+  const long long raw = c1 - c0;
+  long long n = raw < p.max_new ? raw : p.max_new;
+  if (c0 < 0 || c0 > p.n_tokens) n = 0;
+  else if (n > p.n_tokens - c0) n = p.n_tokens - c0;
+  if (n < 0) n = 0;
+  const int kv = max(0, min(kv_in, p.cap));
+  *bad = n != raw || kv != kv_in;
+  Req r;
+  r.row0 = (int)c0;
+  r.n = (int)n;
+  r.pos0 = kv - (int)n;
+  return r;
+}
+
+struct Tile {
+  int row0, tokens, p_first, p_last;           // positions of its first and last token
+  int lo, sinks;                               // its tokens see [0, sinks) and [lo, p_last]
+  int sink_blocks, blocks;                     // blocks before block lo / 128, blocks in all
+};
+
+__device__ __forceinline__ Tile make_tile(const Params& p, const Req& r, int tile) {
+  Tile t;
+  const int t0 = tile * p.tile_tokens;
+  t.row0 = r.row0 + t0;
+  t.tokens = min(p.tile_tokens, r.n - t0);
+  t.p_first = r.pos0 + t0;
+  t.p_last = t.p_first + t.tokens - 1;
+  t.lo = p.window > 0 && t.p_first >= p.window ? t.p_first - p.window + 1 : 0;
+  t.sinks = p.window > 0 ? min(p.sinks, t.lo) : 0;
+  const int b0 = t.lo / kBlock;
+  t.sink_blocks = min((t.sinks + kBlock - 1) / kBlock, b0);
+  // a tile whose tokens see nothing still has one (masked) block: its rows are zeros
+  t.blocks = t.sink_blocks + (t.p_last >= 0 ? t.p_last / kBlock - b0 + 1 : 1);
+  return t;
+}
+
+__device__ __forceinline__ int n_tiles(const Params& p, const Req& r) {
+  return (r.n + p.tile_tokens - 1) / p.tile_tokens;
+}
+
+// One piece of a unit, as the roles of a CTA read it from the ring.
+struct alignas(16) Seg {
+  int b, g, row0, tokens;
+  int p_first, p_last, lo, sinks;
+  int sink_blocks, k0, nb, blocks;             // blocks k0 .. k0+nb-1 of the unit's `blocks`; nb = 0 ends
+  int first_cta, pieces;                       // of a cut unit (pieces = 1 otherwise)
+  int pad0, pad1;
+  __device__ __forceinline__ int key_block(int i) const {   // i counts from k0
+    const int k = k0 + i;
+    return k < sink_blocks ? k : lo / kBlock + (k - sink_blocks);
+  }
+  // Keys [j0, j1] of which no token of the tile sees any.
+  __device__ __forceinline__ bool unseen(int j0, int j1) const {
+    return j0 > p_last || (j1 < lo && j0 >= sinks);
+  }
+  __device__ __forceinline__ bool sees(int j) const { return j <= p_last && (j >= lo || j < sinks); }
+  // Some key of this block is hidden from some token.
+  __device__ __forceinline__ bool masked(const Params& p, int kb) const {
+    const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
+    return j1 > p_first ||
+           (p.window > 0 && p_last >= p.window && j0 <= p_last - p.window && j1 >= p.sinks);
+  }
+  // Some key of this block is hidden from every token.
+  __device__ __forceinline__ bool ragged(int kb) const {
+    const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
+    return j1 > p_last || (j0 < lo && j1 >= sinks);
+  }
+};
+static_assert(sizeof(Seg) == 64, "segments are copied as four uint4");
+
+constexpr int kSegRing = 4;
+
+struct Start {                                 // where a CTA's share begins
+  long long first, end, total;                 // block numbers; total = all blocks
+  int ctas;                                    // CTAs that have a share
+  int b, g, tile, k;
+};
+
+struct SchedSmem {
+  Seg seg[kSegRing];
+  uint64_t full[kSegRing], empty[kSegRing];
+  Start start;
+  long long warp_sum[kWarps];
+};
+
+__device__ __forceinline__ long long warp_sum_ll(long long v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ long long warp_scan_ll(long long v, int lane) {   // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ Req shfl_req(const Req& r, int src) {
+  Req o;
+  o.row0 = __shfl_sync(0xffffffffu, r.row0, src);
+  o.n = __shfl_sync(0xffffffffu, r.n, src);
+  o.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+  return o;
+}
+
+// Blocks of one kv head of the lane's request.  Lanes with few tiles add theirs
+// up alone; a request of many tiles is shared by the warp.
+__device__ __forceinline__ long long head_blocks(const Params& p, const Req& r, int lane) {
+  const int T = n_tiles(p, r);
+  long long w = 0;
+  if (T <= 4)
+    for (int t = 0; t < T; ++t) w += make_tile(p, r, t).blocks;
+  unsigned many = __ballot_sync(0xffffffffu, T > 4);
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    const Req q = shfl_req(r, src);
+    const int Tq = n_tiles(p, q);
+    long long s = 0;
+    for (int t = lane; t < Tq; t += 32) s += make_tile(p, q, t).blocks;
+    s = warp_sum_ll(s);
+    if (lane == src) w = s;
+  }
+  return w;
+}
+
+// Finds the CTA's share (all threads; sm.start is valid after the caller's next
+// __syncthreads).
+__device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.B + kWarps - 1) / kWarps;
+  const int r0 = min(warp * per, p.B), r1 = min(r0 + per, p.B);
+  long long mine = 0, w_first = 0;
+  Req r_first{0, 0, 0};
+  for (int base = r0; base < r1; base += 32) {
+    Req r{0, 0, 0};
+    bool bad = false;
+    if (base + lane < r1) r = load_req(p, base + lane, &bad);
+    if (bad) raise_status(p.status, KS_ERR_INVALID_ARG);
+    const long long w = head_blocks(p, r, lane) * p.Hkv;
+    if (base == r0) {
+      r_first = r;
+      w_first = w;
+    }
+    mine += warp_sum_ll(w);
+  }
+  if (lane == 0) sm.warp_sum[warp] = mine;
+  if (threadIdx.x == 0) sm.start.first = sm.start.end = 0;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) before = total;
+    total += sm.warp_sum[w];
+  }
+  const int ctas = (int)(total < gridDim.x ? total : gridDim.x);
+  const int c = blockIdx.x;
+  if (c >= ctas) return;                       // no share (or no work at all)
+  const long long first = total * c / ctas, end = total * (c + 1) / ctas;
+  if (first < before || first >= before + mine) return;
+  long long at = before;
+  for (int base = r0; base < r1; base += 32) {
+    Req r = r_first;
+    long long w = w_first;
+    if (base != r0) {
+      bool bad;
+      r = Req{0, 0, 0};
+      if (base + lane < r1) r = load_req(p, base + lane, &bad);
+      w = head_blocks(p, r, lane) * p.Hkv;
+    }
+    const long long upto = at + warp_scan_ll(w, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, first < upto);
+    if (!hit) {
+      at = __shfl_sync(0xffffffffu, upto, 31);
+      continue;
+    }
+    const int src = __ffs(hit) - 1;
+    const Req q = shfl_req(r, src);
+    const long long head = __shfl_sync(0xffffffffu, w, src) / p.Hkv;
+    const long long off = first - __shfl_sync(0xffffffffu, upto - w, src);
+    const int g = (int)(off / head), T = n_tiles(p, q);
+    long long rest = off - g * head;
+    for (int t0 = 0; t0 < T; t0 += 32) {
+      const long long nb = t0 + lane < T ? make_tile(p, q, t0 + lane).blocks : 0;
+      const long long s = warp_scan_ll(nb, lane);
+      const unsigned in = __ballot_sync(0xffffffffu, rest < s);
+      if (in) {
+        const int l = __ffs(in) - 1;
+        const int k = (int)(rest - __shfl_sync(0xffffffffu, s - nb, l));
+        if (lane == 0) sm.start = Start{first, end, total, ctas, base + src, g, t0 + l, k};
+        return;
+      }
+      rest -= __shfl_sync(0xffffffffu, s, 31);
+    }
+    return;
+  }
+}
+
+// Warp-uniform wait that also reports a lane's timeout to the others.
+#define KS_PAGED_WAIT(bar, parity) warp_wait(smem_u32(&(bar)), (uint32_t)(parity), abort, p.status)
+
+// The scheduler warp: walks the share and publishes its pieces, then an end mark.
+__device__ __forceinline__ void schedule(const Params& p, SchedSmem& sm, volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  const Start st = sm.start;
+  long long at = st.first;
+  int b = st.b, g = st.g, tile = st.tile, k = st.k;
+  int base = b;                                // lane l holds request base + l
+  bool bad;
+  Req held{0, 0, 0};
+  if (at < st.end && base + lane < p.B) held = load_req(p, base + lane, &bad);
+  uint32_t n = 0;
+  for (;;) {
+    const int slot = n % kSegRing;
+    if (!KS_PAGED_WAIT(sm.empty[slot], ((n / kSegRing) & 1) ^ 1)) return;
+    if (at >= st.end || b >= p.B) {
+      if (lane == 0) {
+        sm.seg[slot].nb = 0;
+        mbar_arrive(smem_u32(&sm.full[slot]));
+      }
+      return;
+    }
+    const Req r = shfl_req(held, b - base);
+    const Tile t = make_tile(p, r, tile);
+    const int nb = (int)(st.end - at < t.blocks - k ? st.end - at : t.blocks - k);
+    if (lane == 0) {
+      Seg s;
+      s.b = b;
+      s.g = g;
+      s.row0 = t.row0;
+      s.tokens = t.tokens;
+      s.p_first = t.p_first;
+      s.p_last = t.p_last;
+      s.lo = t.lo;
+      s.sinks = t.sinks;
+      s.sink_blocks = t.sink_blocks;
+      s.k0 = k;
+      s.nb = nb;
+      s.blocks = t.blocks;
+      s.first_cta = blockIdx.x;
+      s.pieces = 1;
+      s.pad0 = s.pad1 = 0;
+      if (nb < t.blocks) {
+        // block x belongs to CTA ((x + 1) ctas - 1) / total
+        const long long u0 = at - k, u1 = u0 + t.blocks;
+        s.first_cta = (int)(((u0 + 1) * st.ctas - 1) / st.total);
+        s.pieces = (int)((u1 * st.ctas - 1) / st.total) - s.first_cta + 1;
+      }
+      sm.seg[slot] = s;
+      mbar_arrive(smem_u32(&sm.full[slot]));
+    }
+    ++n;
+    at += nb;
+    k = 0;
+    if (++tile == n_tiles(p, r)) {
+      tile = 0;
+      if (++g == p.Hkv) {
+        g = 0;
+        for (++b; b < p.B; ++b) {              // the next request with a token
+          if (b - base == 32) {
+            base = b;
+            held = Req{0, 0, 0};
+            if (base + lane < p.B) held = load_req(p, base + lane, &bad);
+          }
+          if (__shfl_sync(0xffffffffu, held.n, b - base) > 0) break;
+        }
+      }
+    }
+  }
+}
+
+// A role's reader of the ring: take() copies the next piece (false: give up);
+// one lane of each role must be counted in the ring's `empty` barriers.
+struct SegReader {
+  uint32_t n = 0;
+  __device__ __forceinline__ bool take(const Params& p, SchedSmem& sm, volatile int* abort, Seg& s) {
+    const int slot = n % kSegRing;
+    if (!KS_PAGED_WAIT(sm.full[slot], (n / kSegRing) & 1)) return false;
+    const uint4* src = reinterpret_cast<const uint4*>(&sm.seg[slot]);
+    uint4* dst = reinterpret_cast<uint4*>(&s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = src[i];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+    ++n;
+    return true;
+  }
+};
+
+// The pool row (slot) of the first key of this lane's TMA box: lane l loads box
+// l % 16 of panel l / 16.  A box that no token of the tile sees and a page that
+// is none read past the pool, where the tensor map gives zeros without touching
+// memory.  fetch() only loads the table entry, so that it can run a block ahead.
+struct BoxRow {
+  int page, row;                               // row inside the page; -1: unseen
+  __device__ __forceinline__ void fetch(const Params& p, const Seg& s, int kb, int lane) {
+    const int off = (lane & 15) * p.box, j0 = kb * kBlock + off;
+    row = -1;
+    if (off >= kBlock || s.unseen(j0, j0 + p.box - 1)) return;
+    const int blk = j0 / p.page_size;          // a key that is seen lies inside the table's row
+    row = j0 - blk * p.page_size;
+    page = p.table[(long long)s.b * p.max_blocks + blk];
+  }
+  __device__ __forceinline__ int slot(const Params& p) const {
+    if (row < 0) return p.n_slots;
+    if ((unsigned)page < (unsigned)p.n_pages) return page * p.page_size + row;
+    raise_status(p.status, KS_ERR_INVALID_ARG);
+    return p.n_slots;
+  }
+};
+
+// Zeroes the rows of a V block that no token of the tile sees (their weights are
+// zero, but zero times what the page holds there need not be); one warp.
+template <int PANELS>
+__device__ __forceinline__ void zero_unseen(const Seg& s, int kb, unsigned char* v, int lane) {
+  for (int r = lane >> 3; r < kBlock; r += 4)
+    if (!s.sees(kb * kBlock + r))
+#pragma unroll
+      for (int pn = 0; pn < PANELS; ++pn)
+        *reinterpret_cast<uint4*>(v + pn * kBlock * 128 + r * 128 + (lane & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
+__device__ __forceinline__ unsigned char* piece(const Params& p, int cta, int second) {
+  return p.ws + kCounterBytes + (size_t)(2 * cta + second) * kPieceBytes;
+}
+// The piece that this CTA leaves for a segment, and the one that CTA `cta` left.
+__device__ __forceinline__ unsigned char* own_piece(const Params& p, const Seg& s) {
+  return piece(p, blockIdx.x, s.k0 == 0);
+}
+
+// One thread, after every writer of the piece has made it visible and the
+// CTA's writers have met: true for the unit's last arrival.  The counter is
+// zero again afterwards.
+__device__ __forceinline__ bool arrive_piece(const Params& p, const Seg& s) {
+  int* counter = reinterpret_cast<int*>(p.ws) + s.first_cta;
+  __threadfence();
+  const int old = atomicAdd(counter, 1);
+  if (old < 0 || old >= s.pieces) raise_status(p.status, KS_ERR_WORKSPACE);
+  const bool last = old == s.pieces - 1;
+  if (last) *counter = 0;
+  __threadfence();
+  return last;
+}
+
+// Joins a unit's pieces, one row per warp and turn: with M the largest
+// reference, out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, pieces in order.
+template <int HD>
+__device__ __forceinline__ void join_pieces(const Params& p, const Seg& s, int warp, int n_warps,
+                                            int lane) {
+  constexpr int E = HD / 32;
+  const int rows = s.tokens * p.grp;
+  for (int r = warp; r < rows; r += n_warps) {
+    float M = kNoRef, L = 0.f, acc[E] = {};
+    for (int i0 = 0; i0 < s.pieces; i0 += 32)
+      if (i0 + lane < s.pieces)
+        M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(
+                                piece(p, s.first_cta + i0 + lane, i0 + lane == 0)) + r).x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int i0 = 0; i0 < s.pieces; i0 += 32) {
+      float w = 0.f, wl = 0.f;
+      if (i0 + lane < s.pieces) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(
+                                     piece(p, s.first_cta + i0 + lane, i0 + lane == 0)) + r);
+        w = ex2(ml.x - M);
+        wl = w * ml.y;
+      }
+      const int n = min(32, s.pieces - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float* o = reinterpret_cast<const float*>(
+                             piece(p, s.first_cta + i0 + i, i0 + i == 0) + kPieceStats) +
+                         r * HD + lane * E;
+        const float ws = __shfl_sync(0xffffffffu, w, i);
+        L += __shfl_sync(0xffffffffu, wl, i);
+        if (E == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
+          acc[0] += ws * v.x;
+          acc[1] += ws * v.y;
+          acc[E - 2] += ws * v.z;
+          acc[E - 1] += ws * v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+          acc[0] += ws * v.x;
+          acc[1] += ws * v.y;
+        }
+      }
+    }
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const int t = r / p.grp;
+    __nv_bfloat16* dst =
+        p.out + ((long long)(s.row0 + t) * p.Hq + s.g * p.grp + (r - t * p.grp)) * HD + lane * E;
+    uint32_t o[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) o[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[E / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(dst) = o[0];
+  }
+}
+
+}  // namespace paged
+
+// Every request's new tokens in one tile of at most 128 rows.
+ks_status launch_paged_decode(const PagedAttnArgs& a, paged::Params p, int grid, cudaStream_t st);
+
+}  // namespace ks

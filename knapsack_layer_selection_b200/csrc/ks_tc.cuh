@@ -61,6 +61,11 @@ ks_status tc_gemm_groups(const GemmGroupArg* groups, int n_groups, const void* B
 ks_status make_tmap_2d(CUtensorMap* m, const void* base, long long rows, long long cols,
                        long long row_stride, int box_cols, int box_rows);
 
+// Tensor map of bf16 query rows [tokens][heads][hd] read in boxes of box_tokens
+// x box_heads x 64 columns with the 128-byte swizzle.
+ks_status make_tmap_heads(CUtensorMap* m, const void* base, long long tokens, int heads, int hd,
+                          int box_heads, int box_tokens);
+
 // Causal GQA attention on the tensor cores: q, out [R][Hq][hd] bf16 (row r is
 // evaluation token r % T), kc/vc one layer of the cache [cache_rows][Hkv][hd]
 // bf16; token t attends to positions 0 .. ctx + t.  hd = 64 or 128.  With kw,

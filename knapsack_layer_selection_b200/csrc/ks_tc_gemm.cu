@@ -791,6 +791,23 @@ ks_status make_tmap_2d(CUtensorMap* m, const void* base, long long rows, long lo
   return KS_OK;
 }
 
+ks_status make_tmap_heads(CUtensorMap* m, const void* base, long long tokens, int heads, int hd,
+                          int box_heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return fail(KS_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  if ((uintptr_t)base % 16) return fail(KS_ERR_INVALID_ARG, "tensor base not 16-byte aligned");
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)heads * hd * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(KS_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+  return KS_OK;
+}
+
 bool use_tensor_cores(const ks_model_desc* m) { return m->wdtype == KS_BF16; }
 
 ks_status tc_gemm(const void* A, const void* B, const void* B2, void* out, const float* resid,
