@@ -26,6 +26,7 @@ using namespace sm100;
 
 constexpr int kBlock = 128;                  // keys per block
 constexpr int kMaxCtas = 148;                // one CTA per SM of a B200
+constexpr int kTileRows = 128;               // query rows of a tile, at most
 constexpr int kThreads = 384;                // both kernels: 12 warps
 constexpr int kWarps = kThreads / 32;
 constexpr float kNoRef = -1e30f;             // reference of a row that has seen no key
@@ -351,6 +352,16 @@ struct SegReader {
     ++n;
     return true;
   }
+  // The piece in place, for roles without registers to spare; release() gives it back.
+  __device__ __forceinline__ const Seg* peek(const Params& p, SchedSmem& sm, volatile int* abort) {
+    const int slot = n % kSegRing;
+    return KS_PAGED_WAIT(sm.full[slot], (n / kSegRing) & 1) ? &sm.seg[slot] : nullptr;
+  }
+  __device__ __forceinline__ void release(SchedSmem& sm) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.empty[n % kSegRing]));
+    ++n;
+  }
 };
 
 // The pool row (slot) of the first key of this lane's TMA box: lane l loads box
@@ -471,5 +482,8 @@ __device__ __forceinline__ void join_pieces(const Params& p, const Seg& s, int w
 
 // Every request's new tokens in one tile of at most 128 rows.
 ks_status launch_paged_decode(const PagedAttnArgs& a, paged::Params p, int grid, cudaStream_t st);
+// Any step, in tiles of at most 128 rows.
+ks_status launch_paged_chunk(const PagedAttnArgs& a, const paged::Params& p, int grid,
+                             cudaStream_t st);
 
 }  // namespace ks
