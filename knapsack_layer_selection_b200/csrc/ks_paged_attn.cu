@@ -35,7 +35,7 @@ ks_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t st) {
   p.window = a.window < p.cap ? a.window : 0;   // a window that no position outruns hides nothing
   p.sinks = a.n_sinks;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)pool.head_dim));
-  const bool few = (long long)p.grp * p.max_new <= 128;
+  const bool few = (long long)p.grp * p.max_new <= 64;
   p.tile_tokens = few ? p.max_new : paged::kTileRows / p.grp;
   // a CTA per SM, or fewer where the step cannot have as many key blocks
   const long long tiles = (long long)p.B * ceil_div(p.max_new, p.tile_tokens);

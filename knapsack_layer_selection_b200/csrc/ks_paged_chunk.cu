@@ -11,13 +11,15 @@
 // persistent CTA per SM walks an equal share of the step's key blocks
 // (ks_paged_sched.cuh), so that a chunk whose tiles see different numbers of
 // keys, and one with fewer tiles than SMs, still fill the GPU.  384 threads:
-//   warp 0    -- TMA: K blocks into a 3-slot ring, V blocks into a 2-slot ring;
-//                each lane loads the box of one page of one 64-column panel;
+//   warp 0    -- walks the share, publishes its pieces and loads their K blocks
+//                (TMA, 3-slot ring);
 //   warp 1    -- S_i = Q K_i^T; loads the next piece's Q tile itself once its
 //                last S is done, so that no load of K or V waits behind it;
 //   warp 2    -- TMEM owner; [O | l] += P_i [V_i | 1], after zeroing what nobody
 //                sees in a ragged block of V;
-//   warp 3    -- walks the share and publishes its pieces;
+//   warp 3    -- V blocks into a 2-slot ring; in both rings each lane loads the box
+//                of one page of one 64-column panel (issuing a box costs ~57 cycles, so
+//                16-key pages would hold one warp for longer than a block takes);
 //   warps 4-7, 8-11 -- the softmax groups; blocks are numbered over the whole
 //                share, so a piece's first block runs beside its predecessor's last.
 // Registers: a softmax thread holds a block's 128 scores, so the kernel launches
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(smem_u32(&tail->sched.full[s]), 1);
-      mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // TMA, S, P.V and 8 softmax warps
+      mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // V, S, P.V and 8 softmax warps
     }
     mbar_init(smem_u32(&tail->q_full), 1);
     mbar_init(smem_u32(&tail->q_empty), 1);
@@ -138,73 +140,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     regs_dec<C::REGS_LOW>();
-    if (warp == 0) {
-      // ---------------------------------------------------------- TMA
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------------------------------- TMA: K and the walk, V
+      const bool is_k = warp == 0;
+      const CUtensorMap* tm = is_k ? &tmK : &tmV;
+      uint64_t *full = is_k ? tail->k_full : tail->v_full, *empty = is_k ? tail->k_empty : tail->v_empty;
+      const int nst = is_k ? C::KST : C::VST, stride = is_k ? C::KV_BLOCK : C::V_SLOT;
+      const uint32_t off = is_k ? C::OFF_K : C::OFF_V;
+      Walker walk;
       SegReader rd;
-      Seg s;
-      int nk = 0, nv = 0;                      // blocks whose K / V loads were issued
-      int row1 = 0, g1 = 0, row2 = 0, g2 = 0;  // of the last block and the one before it
+      if (is_k) walk.start(p, tail->sched);
+      int n_loads = 0, slot = 0;
+      uint32_t phase = 1;
       bool ok = true;
       const bool mine = (lane & 15) < kBlock / p.box && (lane >> 4) < C::PANELS;
-      const uint32_t box_off = (lane >> 4) * C::KV_PANEL + (lane & 15) * p.box * 128;
-      if (lane == 0) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-      }
-      auto load = [&](const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int m, int nst,
-                      uint32_t off, int row, int g) -> bool {
-        const int sl = m % nst;
-        if (!KS_PAGED_WAIT(empty[sl], ((m / nst) & 1) ^ 1)) return false;
-        const uint32_t fb = smem_u32(&full[sl]);
-        if (lane == 0) mbar_arrive_expect_tx(fb, C::KV_BLOCK);
-        __syncwarp();
-        if (mine) tma_load_2d(sbase + off + box_off, tm, g * HD + (lane >> 4) * 64, row, fb);
-        return true;
-      };
-      auto load_k = [&](int row, int g) -> bool {
-        if (!load(&tmK, tail->k_full, tail->k_empty, nk, C::KST, C::OFF_K + nk % C::KST * C::KV_BLOCK,
-                  row, g))
-          return false;
-        ++nk;
-        return true;
-      };
-      auto load_v = [&](int row, int g) -> bool {
-        if (!load(&tmV, tail->v_full, tail->v_empty, nv, C::VST, C::OFF_V + nv % C::VST * C::V_SLOT,
-                  row, g))
-          return false;
-        ++nv;
-        return true;
-      };
-      // in the order the MMAs consume them: K_0, K_1, then K_{j+2}, V_j for j = 0, 1, ...
+      const uint32_t box_off = sbase + off + (lane >> 4) * C::KV_PANEL + (lane & 15) * p.box * 128;
+      if (lane == 0) prefetch_tmap(tm);
       while (ok) {
-        if (!rd.take(p, tail->sched, abort, s)) break;
-        if (s.nb == 0) {
-          if (nk - nv == 2) ok = load_v(row2, g2);
-          if (ok && nk - nv == 1) load_v(row1, g1);
-          break;
-        }
+        const Seg* s = is_k ? walk.next(p, tail->sched, abort) : rd.peek(p, tail->sched, abort);
+        if (!s || s->nb == 0) break;
+        const int nb = s->nb, x = s->g * HD + (lane >> 4) * 64;
         BoxRow next;
-        next.fetch(p, s, s.key_block(0), lane);
-        for (int i = 0; ok && i < s.nb; ++i) {
+        next.fetch(p, *s, s->key_block(0), lane);
+        for (int i = 0; i < nb; ++i) {
           const BoxRow cur = next;
-          if (i + 1 < s.nb) next.fetch(p, s, s.key_block(i + 1), lane);
-          const int row = cur.slot(p);
-          ok = load_k(row, s.g);
-          if (ok && nk - nv == 3) ok = load_v(row2, g2);
-          row2 = row1;
-          g2 = g1;
-          row1 = row;
-          g1 = s.g;
+          if (i + 1 < nb) next.fetch(p, *s, s->key_block(i + 1), lane);
+          if (!(ok = KS_PAGED_WAIT(empty[slot], phase))) break;
+          const uint32_t fb = smem_u32(&full[slot]);
+          if (lane == 0) mbar_arrive_expect_tx(fb, C::KV_BLOCK);
+          __syncwarp();
+          if (mine) tma_load_2d(box_off + slot * stride, tm, x, cur.slot(p), fb);
+          ++n_loads;
+          if (++slot == nst) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
+        if (!is_k) rd.release(tail->sched);
       }
       // drain the copies still in flight before leaving
-      if (lane == 0) {
-        for (int i = nk > C::KST ? nk - C::KST : 0; i < nk; ++i)
-          mbar_wait_drain(smem_u32(&tail->k_full[i % C::KST]), (uint32_t)(i / C::KST) & 1u, p.status);
-        for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i)
-          mbar_wait_drain(smem_u32(&tail->v_full[i % C::VST]), (uint32_t)(i / C::VST) & 1u, p.status);
-      }
+      if (lane == 0)
+        for (int i = n_loads > nst ? n_loads - nst : 0; i < n_loads; ++i)
+          mbar_wait_drain(smem_u32(&full[i % nst]), (uint32_t)(i / nst) & 1u, p.status);
     } else if (warp == 1) {
       // ---------------------------------------------------------- Q loads and S
       SegReader rd;
@@ -214,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kph = 0;
       bool ok = true;
       const int box_rows = p.grp * p.tile_tokens;
+      if (lane == 0) prefetch_tmap(&tmQ);
       const uint64_t dq0 = desc_kmajor_sw128(sbase);
       const uint64_t dk0 = desc_kmajor_sw128(sbase + C::OFF_K);
       while (ok) {
@@ -294,8 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(smem_u32(&tail->drain[1]));
         mbar_wait_drain(smem_u32(&tail->drain[1]), 0, p.status);
       }
-    } else {
-      schedule(p, tail->sched, abort);
     }
   } else {
     regs_inc<C::REGS_HIGH>();

@@ -1,10 +1,10 @@
-// Attention over the paged cache for up to 128 query rows per request and kv
+// Attention over the paged cache for up to 64 query rows per request and kv
 // head: one token each (a drafting step), a few (a verification), a short chunk
 // (sm_100a, tcgen05 + TMEM + TMA).
 //
 // Every key and value is read once, and a row of them meets few queries, so the
 // keys' traffic bounds it.  The products are turned round so that the keys fill
-// the tensor core's 128 rows and the queries are its (16 .. 128) columns:
+// the tensor core's 128 rows and the queries are its (16 .. 64) columns:
 //   S^T = K Q^T      A = K block [128 keys][hd],       B = Q [rows][hd]
 //   O^T += V^T P^T   A = V block read MN-major [hd][128], B = P [rows][128 keys]
 // A thread of the softmax is then a key, and its work is one exponential per
@@ -13,14 +13,17 @@
 //
 // One persistent CTA per SM takes an equal share of the step's key blocks
 // (ks_paged_sched.cuh); 384 threads:
-//   warp 0    -- TMA: per piece its Q tile (two buffers), and one ring of 128-key
-//                tiles in the order K_0, K_1, V_0, K_2, V_1, ...; each lane loads
-//                the box of one page (the largest power of two of keys, up to
-//                128, that divides the page) of one 64-column panel;
-//   warp 1    -- S_{i+1}, then P.V_i, for the whole share: across pieces too, so
-//                a short piece's tail hides the next one's first products;
-//   warp 2    -- TMEM owner;
-//   warp 3    -- walks the share and publishes its pieces;
+//   warp 0    -- walks the share, publishes its pieces, loads their Q (two
+//                buffers) and K blocks (TMA, a ring);
+//   warp 2    -- TMEM owner; V blocks into a ring of their own.  In both rings each
+//                lane loads the box of one page (the largest power of two of keys,
+//                up to 128, that divides the page) of one 64-column panel; issuing
+//                a box costs ~57 cycles, so 16-key pages would hold a single warp
+//                for longer than a block's bytes take;
+//   warp 1    -- S_i; warp 3 -- P.V_i: an issue of eight products with its waits and
+//                commits takes ~750 cycles, so one warp for both would be the
+//                bottleneck.  Blocks are numbered over the whole share: a short
+//                piece's tail runs beside its successor's first products;
 //   warps 4-11 -- two softmax groups, each half of the query rows (TMEM columns),
 //                thread = key.  P goes to shared memory (two buffers).
 // The softmax reference of a row is kept until a score exceeds it by 2^8, so a
@@ -40,20 +43,19 @@ using namespace paged;
 
 namespace {
 
-constexpr int kMaxRing = 12;
+constexpr int kMaxRing = 6;                    // slots of the K ring, and of the V ring
 constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 118784;             // one CTA holds an SM and its 512 TMEM columns
 
 struct Tail {
   SchedSmem sched;
-  uint64_t full[kMaxRing], empty[kMaxRing];
+  uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];   // by block parity
   uint64_t o_free;                                        // one phase per piece
-  uint64_t gsync[2], esync, drain;                        // meetings of a group's / all softmax warps
+  uint64_t esync, drain[2];                               // meetings of all softmax warps; MMA drains
   uint32_t tmem_base;
   int abort, last;
-  alignas(16) int vote[2][2][4];                                 // [group][block parity][warp]
   alignas(16) float nref[128], alpha[128];                // -reference and rescale factor by row
   float wmax[4][128], lsum[4][128];                       // by warp and row
 };
@@ -121,20 +123,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int N = p.q_rows, row_panel = N * 128;           // a 64-column panel of N rows
   const int q_tile = PANELS * row_panel, p_tile = 2 * row_panel;
-  const int off_q = p.n_slots_ring * SLOT, off_p = off_q + p.q_bufs * q_tile;
+  const int off_v = p.k_slots * SLOT, off_q = off_v + p.v_slots * SLOT, off_p = off_q + 2 * q_tile;
   Tail* tail = reinterpret_cast<Tail*>(smem + off_p + 2 * p_tile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &tail->abort;
   const uint32_t sbase = smem_u32(smem);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.n_slots_ring; ++s) {
-      mbar_init(smem_u32(&tail->full[s]), 1);
-      mbar_init(smem_u32(&tail->empty[s]), 1);
+    for (int s = 0; s < kMaxRing; ++s) {
+      mbar_init(smem_u32(&tail->k_full[s]), 1);
+      mbar_init(smem_u32(&tail->k_empty[s]), 1);
+      mbar_init(smem_u32(&tail->v_full[s]), 1);
+      mbar_init(smem_u32(&tail->v_empty[s]), 1);
     }
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(smem_u32(&tail->sched.full[s]), 1);
-      mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // TMA, S, P.V and 8 softmax warps
+      mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // V, S, P.V and 8 softmax warps
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tail->q_full[b]), 1);
@@ -143,11 +147,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&tail->s_free[b]), 8);
       mbar_init(smem_u32(&tail->p_full[b]), 8);
       mbar_init(smem_u32(&tail->pv_done[b]), 1);
-      mbar_init(smem_u32(&tail->gsync[b]), 4);
     }
     mbar_init(smem_u32(&tail->o_free), 8);
     mbar_init(smem_u32(&tail->esync), 8);
-    mbar_init(smem_u32(&tail->drain), 1);
+    mbar_init(smem_u32(&tail->drain[0]), 1);
+    mbar_init(smem_u32(&tail->drain[1]), 1);
     tail->abort = 0;
     fence_barrier_init();
   }
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // rows of a Q tile that no load writes (the tile's rows rounded up to 16)
   const int box_rows = p.grp * p.tile_tokens;
-  for (int e = threadIdx.x; e < p.q_bufs * PANELS * (N - box_rows) * 8; e += kThreads) {
+  for (int e = threadIdx.x; e < 2 * PANELS * (N - box_rows) * 8; e += kThreads) {
     const int pn = e / ((N - box_rows) * 8), o = e - pn * ((N - box_rows) * 8);
     reinterpret_cast<uint4*>(smem + off_q + pn * row_panel + box_rows * 128)[o] =
         make_uint4(0, 0, 0, 0);
@@ -170,166 +174,159 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tail->tmem_base;
   constexpr uint32_t kS = 0, kO = 256;         // TMEM columns: S[b] at 128 b, then O
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA: the walk, Q and K; V
+    const bool is_k = warp == 0;
+    const CUtensorMap* tm = is_k ? &tmK : &tmV;
+    uint64_t *full = is_k ? tail->k_full : tail->v_full, *empty = is_k ? tail->k_empty : tail->v_empty;
+    const int nst = is_k ? p.k_slots : p.v_slots;
+    const uint32_t base = sbase + (is_k ? 0 : off_v);
+    Walker walk;
     SegReader rd;
-    Seg s;
-    int slot = 0, n_loads = 0, prev_row = 0, prev_g = 0, n_seg = 0;
+    if (is_k) walk.start(p, tail->sched);
+    int n_loads = 0, slot = 0, n_seg = 0;
     uint32_t phase = 1;
-    bool ok = true, have_prev = false;
-    const int nbox = kBlock / p.box;
-    const bool mine = (lane & 15) < nbox && (lane >> 4) < PANELS;
-    const uint32_t box_off = (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
+    bool ok = true;
+    const bool mine = (lane & 15) < kBlock / p.box && (lane >> 4) < PANELS;
+    const uint32_t box_off = base + (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
     if (lane == 0) {
-      prefetch_tmap(&tmQ);
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
+      prefetch_tmap(tm);
+      if (is_k) prefetch_tmap(&tmQ);
     }
-    auto load = [&](const CUtensorMap* tm, int row, int g) -> bool {
-      if (!KS_PAGED_WAIT(tail->empty[slot], phase)) return false;
-      const uint32_t fb = smem_u32(&tail->full[slot]);
-      if (lane == 0) mbar_arrive_expect_tx(fb, SLOT);
-      __syncwarp();
-      if (mine) tma_load_2d(sbase + slot * SLOT + box_off, tm, g * HD + (lane >> 4) * 64, row, fb);
-      ++n_loads;
-      if (++slot == p.n_slots_ring) {
-        slot = 0;
-        phase ^= 1;
-      }
-      return true;
-    };
     while (ok) {
-      if (!rd.take(p, tail->sched, abort, s)) break;
-      if (s.nb == 0) {
-        if (have_prev) load(&tmV, prev_row, prev_g);
-        break;
-      }
+      const Seg* s = is_k ? walk.next(p, tail->sched, abort) : rd.peek(p, tail->sched, abort);
+      if (!s || s->nb == 0) break;
+      const int nb = s->nb, x = s->g * HD + (lane >> 4) * 64;
       BoxRow next;
-      next.fetch(p, s, s.key_block(0), lane);
-      const int qb = n_seg % p.q_bufs;
-      if (!KS_PAGED_WAIT(tail->q_empty[qb], ((n_seg / p.q_bufs) & 1) ^ 1)) break;
-      if (lane == 0) {
-        const uint32_t qf = smem_u32(&tail->q_full[qb]);
-        mbar_arrive_expect_tx(qf, PANELS * box_rows * 128);
-        for (int pn = 0; pn < PANELS; ++pn)
-          tma_load_3d(sbase + off_q + qb * q_tile + pn * row_panel, &tmQ, pn * 64, s.g * p.grp,
-                      s.row0, qf);
+      next.fetch(p, *s, s->key_block(0), lane);
+      if (is_k) {
+        const int qb = n_seg & 1;
+        if (!(ok = KS_PAGED_WAIT(tail->q_empty[qb], ((n_seg >> 1) & 1) ^ 1))) break;
+        if (lane == 0) {
+          const uint32_t qf = smem_u32(&tail->q_full[qb]);
+          mbar_arrive_expect_tx(qf, PANELS * box_rows * 128);
+          for (int pn = 0; pn < PANELS; ++pn)
+            tma_load_3d(sbase + off_q + qb * q_tile + pn * row_panel, &tmQ, pn * 64, s->g * p.grp,
+                        s->row0, qf);
+        }
+        __syncwarp();
+        ++n_seg;
       }
-      ++n_seg;
-      for (int i = 0; ok && i < s.nb; ++i) {
+      for (int i = 0; i < nb; ++i) {
         const BoxRow cur = next;
-        if (i + 1 < s.nb) next.fetch(p, s, s.key_block(i + 1), lane);
-        const int row = cur.slot(p);
-        ok = load(&tmK, row, s.g);
-        if (ok && have_prev) ok = load(&tmV, prev_row, prev_g);
-        prev_row = row;
-        prev_g = s.g;
-        have_prev = true;
+        if (i + 1 < nb) next.fetch(p, *s, s->key_block(i + 1), lane);
+        if (!(ok = KS_PAGED_WAIT(empty[slot], phase))) break;
+        const uint32_t fb = smem_u32(&full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(fb, SLOT);
+        __syncwarp();
+        if (mine) tma_load_2d(box_off + slot * SLOT, tm, x, cur.slot(p), fb);
+        ++n_loads;
+        if (++slot == nst) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
+      if (!is_k) rd.release(tail->sched);
     }
     // drain the copies still in flight before leaving
     if (lane == 0) {
-      for (int n = n_seg > p.q_bufs ? n_seg - p.q_bufs : 0; n < n_seg; ++n)
-        mbar_wait_drain(smem_u32(&tail->q_full[n % p.q_bufs]), (n / p.q_bufs) & 1, p.status);
-      for (int n = n_loads > p.n_slots_ring ? n_loads - p.n_slots_ring : 0; n < n_loads; ++n)
-        mbar_wait_drain(smem_u32(&tail->full[n % p.n_slots_ring]),
-                        (uint32_t)(n / p.n_slots_ring) & 1, p.status);
+      for (int n = n_seg > 2 ? n_seg - 2 : 0; n < n_seg; ++n)
+        mbar_wait_drain(smem_u32(&tail->q_full[n & 1]), (n >> 1) & 1, p.status);
+      for (int n = n_loads > nst ? n_loads - nst : 0; n < n_loads; ++n)
+        mbar_wait_drain(smem_u32(&full[n % nst]), (uint32_t)(n / nst) & 1, p.status);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    SegReader rs, rp;                          // the pieces of S, and those of P.V behind it
-    Seg ss, sp;
-    ss.nb = sp.nb = 0;
-    int si = 0, pi = 0, slot = 0, s_segs = 0, qb = 0;
-    uint32_t phase = 0, i = 0, j = 0, p_segs = 0;
-    bool s_end = false;
-    const uint32_t idesc_s = idesc_bf16_f32(128, N);
-    const uint32_t idesc_o = idesc_bf16_f32(128, N) | (1u << 15);   // A (V) MN-major
+    // ------------------------------------------------------------ S_i = K_i Q^T
+    SegReader rd;
+    int slot = 0;
+    uint32_t phase = 0, i = 0, n_seg = 0;
+    bool ok = true;
+    const uint32_t idesc = idesc_bf16_f32(128, N);
     const uint64_t dk0 = desc_kmajor_sw128(sbase), dq0 = desc_kmajor_sw128(sbase + off_q);
+    const uint32_t rp16 = row_panel >> 4;
+    while (ok) {
+      const Seg* s = rd.peek(p, tail->sched, abort);
+      const int nb = s ? s->nb : 0;
+      if (nb == 0) break;
+      rd.release(tail->sched);
+      const uint32_t qb = n_seg & 1;
+      ok = KS_PAGED_WAIT(tail->q_full[qb], (n_seg >> 1) & 1);
+      ++n_seg;
+      for (int e = 0; ok && e < nb; ++e, ++i) {
+        // into S buffer i % 2, free once the softmax has copied S_{i-2}
+        const uint32_t b = i & 1;
+        if (i >= 2 && !(ok = KS_PAGED_WAIT(tail->s_free[b], ((i - 2) >> 1) & 1))) break;
+        if (!(ok = KS_PAGED_WAIT(tail->k_full[slot], phase))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dk = dk0 + (uint64_t)((slot * SLOT) >> 4);
+          const uint64_t dq = dq0 + (uint64_t)((qb * q_tile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_bf16(tmem + kS + b * 128, dk + (uint64_t)((kk / 4) * ((kBlock * 128) >> 4) + 2 * (kk % 4)),
+                     dq + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, kk > 0);
+          // one commit: the softmax warp that sees S_i complete frees K_i's slot
+          mma_commit(smem_u32(&tail->s_full[b]));
+          if (e == nb - 1) mma_commit(smem_u32(&tail->q_empty[qb]));
+        }
+        __syncwarp();
+        if (++slot == p.k_slots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (lane == 0) {
+      mma_commit(smem_u32(&tail->drain[0]));
+      mbar_wait_drain(smem_u32(&tail->drain[0]), 0, p.status);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ O^T += V_i^T P_i
+    SegReader rd;
+    Seg s;
+    int slot = 0;
+    uint32_t phase = 0, i = 0, n_seg = 0;
+    bool ok = true;
+    const uint32_t idesc = idesc_bf16_f32(128, N) | (1u << 15);   // A (V) MN-major
     const uint64_t dp0 = desc_kmajor_sw128(sbase + off_p);
     // head_dim 64: rows 64 .. 127 of the product repeat V's columns some keys further on; nobody
     // reads them
-    const uint64_t dv0 = desc_mnmajor_sw128(sbase, PANELS == 2 ? kBlock * 128 : 1024);
+    const uint64_t dv0 = desc_mnmajor_sw128(sbase + off_v, PANELS == 2 ? kBlock * 128 : 1024);
     const uint32_t rp16 = row_panel >> 4;
-    auto step_ring = [&] {
-      if (++slot == p.n_slots_ring) {
-        slot = 0;
-        phase ^= 1;
-      }
-    };
-    // S_i = K_i Q^T into S buffer i % 2, free once the softmax has copied S_{i-2}
-    auto issue_s = [&]() -> bool {
-      if (s_end) return true;
-      if (si == ss.nb) {
-        if (!rs.take(p, tail->sched, abort, ss)) return false;
-        si = 0;
-        if (ss.nb == 0) {
-          s_end = true;
-          return true;
+    while (ok) {
+      if (!rd.take(p, tail->sched, abort, s) || s.nb == 0) break;
+      // O still holds the piece before this one until its rows have been read
+      if (n_seg > 0 && !KS_PAGED_WAIT(tail->o_free, (n_seg - 1) & 1)) break;
+      ++n_seg;
+      for (int e = 0; e < s.nb; ++e, ++i) {
+        const uint32_t b = i & 1;
+        const int kb = s.key_block(e);
+        if (!(ok = KS_PAGED_WAIT(tail->v_full[slot], phase))) break;
+        if (s.ragged(kb)) zero_unseen<PANELS>(s, kb, smem + off_v + slot * SLOT, lane);
+        if (!(ok = KS_PAGED_WAIT(tail->p_full[b], (i >> 1) & 1))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dv = dv0 + (uint64_t)((slot * SLOT) >> 4);
+          const uint64_t dp = dp0 + (uint64_t)((b * p_tile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            mma_bf16(tmem + kO, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
+                     dp + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, e > 0 || kk > 0);
+          mma_commit(smem_u32(&tail->v_empty[slot]));
+          mma_commit(smem_u32(&tail->pv_done[b]));
         }
-        qb = s_segs % p.q_bufs;
-        if (!KS_PAGED_WAIT(tail->q_full[qb], (s_segs / p.q_bufs) & 1)) return false;
-        ++s_segs;
+        __syncwarp();
+        if (++slot == p.v_slots) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
-      const uint32_t b = i & 1;
-      if (i >= 2 && !KS_PAGED_WAIT(tail->s_free[b], ((i - 2) >> 1) & 1)) return false;
-      if (!KS_PAGED_WAIT(tail->full[slot], phase)) return false;
-      tc_fence_after();
-      ++si;
-      if (lane == 0) {
-        const uint64_t dk = dk0 + (uint64_t)((slot * SLOT) >> 4);
-        const uint64_t dq = dq0 + (uint64_t)((qb * q_tile) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          mma_bf16(tmem + kS + b * 128, dk + (uint64_t)((kk / 4) * ((kBlock * 128) >> 4) + 2 * (kk % 4)),
-                   dq + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc_s, kk > 0);
-        mma_commit(smem_u32(&tail->s_full[b]));
-        mma_commit(smem_u32(&tail->empty[slot]));
-        if (si == ss.nb) mma_commit(smem_u32(&tail->q_empty[qb]));
-      }
-      __syncwarp();
-      step_ring();
-      ++i;
-      return true;
-    };
-    bool ok = issue_s();
-    while (ok && (ok = issue_s())) {
-      // O^T += V_j^T P_j once the softmax has written P_j
-      if (pi == sp.nb) {
-        if (!rp.take(p, tail->sched, abort, sp)) break;
-        if (sp.nb == 0) break;
-        pi = 0;
-        if (p_segs > 0 && !KS_PAGED_WAIT(tail->o_free, (p_segs - 1) & 1)) break;
-        ++p_segs;
-      }
-      const uint32_t b = j & 1;
-      if (!KS_PAGED_WAIT(tail->full[slot], phase)) break;
-      const int kb = sp.key_block(pi);
-      if (sp.ragged(kb)) zero_unseen<PANELS>(sp, kb, smem + slot * SLOT, lane);
-      if (!KS_PAGED_WAIT(tail->p_full[b], (j >> 1) & 1)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t dv = dv0 + (uint64_t)((slot * SLOT) >> 4);
-        const uint64_t dp = dp0 + (uint64_t)((b * p_tile) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk)
-          mma_bf16(tmem + kO, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
-                   dp + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc_o, pi > 0 || kk > 0);
-        mma_commit(smem_u32(&tail->pv_done[b]));
-        mma_commit(smem_u32(&tail->empty[slot]));
-      }
-      __syncwarp();
-      step_ring();
-      ++pi;
-      ++j;
     }
     if (lane == 0) {
-      mma_commit(smem_u32(&tail->drain));
-      mbar_wait_drain(smem_u32(&tail->drain), 0, p.status);
+      mma_commit(smem_u32(&tail->drain[1]));
+      mbar_wait_drain(smem_u32(&tail->drain[1]), 0, p.status);
     }
-  } else if (warp == 3) {
-    schedule(p, tail->sched, abort);
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax
     const int G = (warp - 4) >> 2, q4 = warp & 3;
     const int key = q4 * 32 + lane;            // key of the block = TMEM lane
@@ -340,13 +337,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_chunk = (key & 63) >> 3;
     SegReader rd;
     Seg s;
-    uint32_t j = 0, syncs = 0, esyncs = 0;
+    uint32_t j = 0, esyncs = 0;
+    int k_slot = 0;
     bool ok = true;
-    auto meet = [&]() -> bool {                // the group's four warps
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tail->gsync[G]));
-      return KS_PAGED_WAIT(tail->gsync[G], syncs++ & 1);
+    // The group's four warps meet at a hardware barrier (a tenth of an mbarrier's latency) and
+    // vote: the count is 0, 1 .. 4 when some of them ask for new references, 32 or more when one
+    // has given up.  A barrier has no time limit, so a warp that leaves, for whatever reason but
+    // such a vote, comes to one more: its partners are then never left waiting.
+    bool voted_out = false, finished = false;
+    auto vote = [&](bool mine) -> int {
+      int n;
+      asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                   "bar.red.popc.u32 %0, %1, 128, q;\n\t}"
+                   : "=r"(n)
+                   : "r"(1 + G), "r"((int)mine)
+                   : "memory");
+      voted_out = n >= 32;
+      return n;
     };
+    auto meet = [&]() -> bool { return vote(false) < 32; };
     auto meet_all = [&]() -> bool {            // all eight
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail->esync));
@@ -360,7 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     while (ok) {
-      if (!rd.take(p, tail->sched, abort, s) || s.nb == 0) break;
+      if (!rd.take(p, tail->sched, abort, s)) break;
+      if (s.nb == 0) {
+        finished = true;
+        break;
+      }
       const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
       const int r0 = G ? half * 8 : 0;         // this group's first row
       const int nch = G ? chunks - half : half;
@@ -373,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        if (warp == 4 && lane == 0) mbar_arrive(smem_u32(&tail->k_empty[k_slot]));   // K_j read
+        if (++k_slot == p.k_slots) k_slot = 0;
         tc_fence_after();
         float sc[CPG];
 #pragma unroll
@@ -416,13 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
               }
             any = __any_sync(0xffffffffu, any);
-            if (lane == 0) tail->vote[G][b][q4] = any;
-            if (!meet()) {
+            const int n = vote(any && lane == 0);
+            if (n >= 32) {
               ok = false;
               break;
             }
-            const int4 v = *reinterpret_cast<const int4*>(tail->vote[G][b]);
-            grow = v.x | v.y | v.z | v.w;
+            grow = n > 0;
           }
           if (grow) {
             // maxima over the keys, and the rows' new references
@@ -571,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (!voted_out) vote(!finished);
   }
 
   tc_fence_before();
@@ -590,12 +605,11 @@ ks_status launch(Params p, const CUtensorMap& tq, const CUtensorMap& tk, const C
     KS_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
     return KS_OK;
   }));
-  // a second Q buffer lets a piece's first product follow the last one's at once; above 64 rows its
-  // room is worth more as a fifth ring slot
-  p.q_bufs = p.q_rows <= 64 ? 2 : 1;
-  const int tiles = (p.q_bufs * (HD / 64) + 4) * p.q_rows * 128 + kTailBytes;   // Q, P and the rest
-  p.n_slots_ring = std::min(kMaxRing, (kSmemLimit - tiles) / slot_bytes<HD>());
-  const int smem = std::max(kSmemFloor, p.n_slots_ring * slot_bytes<HD>() + tiles);
+  const int tiles = (2 * (HD / 64) + 4) * p.q_rows * 128 + kTailBytes;   // Q, P and the rest
+  const int slots = std::min(2 * kMaxRing, (kSmemLimit - tiles) / slot_bytes<HD>());
+  p.v_slots = (slots + 1) / 2;                 // a V block waits for its P, a K block for nothing
+  p.k_slots = slots / 2;
+  const int smem = std::max(kSmemFloor, slots * slot_bytes<HD>() + tiles);
   k<<<grid, kThreads, smem, st>>>(tq, tk, tv, p);
   KS_LAUNCH_CHECK();
   return KS_OK;
@@ -607,8 +621,7 @@ ks_status launch_hd(const Params& p, const CUtensorMap& tq, const CUtensorMap& t
   const int rows = p.grp * p.tile_tokens;
   if (rows <= 16) return launch<HD, 8>(p, tq, tk, tv, grid, st);
   if (rows <= 32) return launch<HD, 16>(p, tq, tk, tv, grid, st);
-  if (rows <= 64) return launch<HD, 32>(p, tq, tk, tv, grid, st);
-  return launch<HD, 64>(p, tq, tk, tv, grid, st);
+  return launch<HD, 32>(p, tq, tk, tv, grid, st);
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ struct Params {
   int window, sinks;
   int tile_tokens;                             // tokens per query tile
   int q_rows;                                  // decode kernel: rows of a Q / P tile (N)
-  int n_slots_ring, q_bufs;                    // decode kernel: ring slots, Q buffers
+  int k_slots, v_slots;                        // decode kernel: ring slots
   float scale_log2;
 };
 
@@ -266,30 +266,46 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
 // Warp-uniform wait that also reports a lane's timeout to the others.
 #define KS_PAGED_WAIT(bar, parity) warp_wait(smem_u32(&(bar)), (uint32_t)(parity), abort, p.status)
 
-// The scheduler warp: walks the share and publishes its pieces, then an end mark.
-__device__ __forceinline__ void schedule(const Params& p, SchedSmem& sm, volatile int* abort) {
-  const int lane = threadIdx.x & 31;
-  const Start st = sm.start;
-  long long at = st.first;
-  int b = st.b, g = st.g, tile = st.tile, k = st.k;
-  int base = b;                                // lane l holds request base + l
-  bool bad;
-  Req held{0, 0, 0};
-  if (at < st.end && base + lane < p.B) held = load_req(p, base + lane, &bad);
-  uint32_t n = 0;
-  for (;;) {
-    const int slot = n % kSegRing;
-    if (!KS_PAGED_WAIT(sm.empty[slot], ((n / kSegRing) & 1) ^ 1)) return;
-    if (at >= st.end || b >= p.B) {
+// Walks a CTA's share and publishes its pieces, then an end mark (one warp, which
+// also loads the keys: a piece is published when its first key block is next).
+struct Walker {
+  long long at;
+  int b, g, tile, k, base;
+  Req held;                                    // lane l holds request base + l
+  uint32_t n;
+  __device__ __forceinline__ void hold(const Params& p) {
+    const int r = base + (threadIdx.x & 31);
+    bool bad;
+    held = Req{0, 0, 0};
+    if (r < p.B) held = load_req(p, r, &bad);
+  }
+  __device__ __forceinline__ void start(const Params& p, const SchedSmem& sm) {
+    at = sm.start.first;
+    b = base = sm.start.b;
+    g = sm.start.g;
+    tile = sm.start.tile;
+    k = sm.start.k;
+    n = 0;
+    if (at < sm.start.end) hold(p);
+  }
+  // The next piece in the ring (nb = 0: the end), or NULL to give up.
+  __device__ __forceinline__ const Seg* next(const Params& p, SchedSmem& sm, volatile int* abort) {
+    const int lane = threadIdx.x & 31, slot = n % kSegRing;
+    if (!KS_PAGED_WAIT(sm.empty[slot], ((n / kSegRing) & 1) ^ 1)) return nullptr;
+    ++n;
+    Seg* seg = &sm.seg[slot];
+    const long long end = sm.start.end;
+    if (at >= end || b >= p.B) {
       if (lane == 0) {
-        sm.seg[slot].nb = 0;
+        seg->nb = 0;
         mbar_arrive(smem_u32(&sm.full[slot]));
       }
-      return;
+      __syncwarp();
+      return seg;
     }
     const Req r = shfl_req(held, b - base);
     const Tile t = make_tile(p, r, tile);
-    const int nb = (int)(st.end - at < t.blocks - k ? st.end - at : t.blocks - k);
+    const int nb = (int)(end - at < t.blocks - k ? end - at : t.blocks - k);
     if (lane == 0) {
       Seg s;
       s.b = b;
@@ -309,14 +325,15 @@ __device__ __forceinline__ void schedule(const Params& p, SchedSmem& sm, volatil
       s.pad0 = s.pad1 = 0;
       if (nb < t.blocks) {
         // block x belongs to CTA ((x + 1) ctas - 1) / total
-        const long long u0 = at - k, u1 = u0 + t.blocks;
-        s.first_cta = (int)(((u0 + 1) * st.ctas - 1) / st.total);
-        s.pieces = (int)((u1 * st.ctas - 1) / st.total) - s.first_cta + 1;
+        const long long u0 = at - k, u1 = u0 + t.blocks, total = sm.start.total;
+        const int ctas = sm.start.ctas;
+        s.first_cta = (int)(((u0 + 1) * ctas - 1) / total);
+        s.pieces = (int)((u1 * ctas - 1) / total) - s.first_cta + 1;
       }
-      sm.seg[slot] = s;
+      *seg = s;
       mbar_arrive(smem_u32(&sm.full[slot]));
     }
-    ++n;
+    __syncwarp();
     at += nb;
     k = 0;
     if (++tile == n_tiles(p, r)) {
@@ -326,15 +343,15 @@ __device__ __forceinline__ void schedule(const Params& p, SchedSmem& sm, volatil
         for (++b; b < p.B; ++b) {              // the next request with a token
           if (b - base == 32) {
             base = b;
-            held = Req{0, 0, 0};
-            if (base + lane < p.B) held = load_req(p, base + lane, &bad);
+            hold(p);
           }
           if (__shfl_sync(0xffffffffu, held.n, b - base) > 0) break;
         }
       }
     }
+    return seg;
   }
-}
+};
 
 // A role's reader of the ring: take() copies the next piece (false: give up);
 // one lane of each role must be counted in the ring's `empty` barriers.
@@ -480,7 +497,7 @@ __device__ __forceinline__ void join_pieces(const Params& p, const Seg& s, int w
 
 }  // namespace paged
 
-// Every request's new tokens in one tile of at most 128 rows.
+// Every request's new tokens in one tile of at most 64 rows.
 ks_status launch_paged_decode(const PagedAttnArgs& a, paged::Params p, int grid, cudaStream_t st);
 // Any step, in tiles of at most 128 rows.
 ks_status launch_paged_chunk(const PagedAttnArgs& a, const paged::Params& p, int grid,
