@@ -383,6 +383,44 @@ def attention_bf16(q: torch.Tensor, k_layer: torch.Tensor, v_layer: torch.Tensor
 
 
 # ---------------------------------------------------------------- paged cache
+# These run once per layer and step on inputs of a few kilobytes, so a call's
+# checks are a good part of it: one look at the current device, and per tensor
+# the cheap tests first, the explaining ones only when those fail.
+_I32, _BF16 = torch.int32, torch.bfloat16
+
+
+def _device(t: torch.Tensor) -> int:
+    """The current device, for a call on t (-2, which no tensor is on, if t is on the CPU)."""
+    return torch.cuda.current_device() if t.is_cuda else -2
+
+
+# the current stream's handle without building a Stream object (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev: int) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else _stream()
+
+
+def _ptr(t: torch.Tensor, dtype, name: str, dev: int) -> int:
+    if t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, dtype, name)
+
+
+def _status_ptr(status: Optional[torch.Tensor], dev: int) -> Optional[int]:
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise KnapSpecError("status must hold one int32")
+    return _ptr(status, _I32, "status", dev)
+
+
+def _same(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if t.shape != shape:
+        raise KnapSpecError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
 def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
               block_table: torch.Tensor, page_size: int, n_pages: int, cu_new: torch.Tensor,
               kv_len: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -390,58 +428,55 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Te
     """A step's layout from the requests' lengths (ks_page_plan), all int32:
     ctx_len, new_len, kv_len [B], free_pages [n], block_table [B][max_blocks]
     (updated in place), cu_new [B+1], positions, slots [max_tokens], n_taken [1]."""
-    B = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
-    _shape(ctx_len, (B,), "ctx_len")
-    _shape(new_len, (B,), "new_len")
-    _shape(kv_len, (B,), "kv_len")
-    _shape(cu_new, (B + 1,), "cu_new")
-    _shape(n_taken, (1,), "n_taken")
+    row = ctx_len.shape
+    if len(row) != 1:
+        raise KnapSpecError(f"ctx_len must be [B], got {tuple(row)}")
+    B = row[0]
+    _same(new_len, row, "new_len")
+    _same(kv_len, row, "kv_len")
+    _same(cu_new, (B + 1,), "cu_new")
+    _same(n_taken, (1,), "n_taken")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise KnapSpecError(f"block_table must be [{B}][max_blocks], got {tuple(block_table.shape)}")
     n_free, cap = free_pages.numel(), positions.numel()
-    _shape(free_pages, (n_free,), "free_pages")
-    _shape(positions, (cap,), "positions")
-    _shape(slots, (cap,), "slots")
-    if status is not None and status.numel() < 1:
-        raise KnapSpecError("status must hold one int32")
-    i32 = torch.int32
-    _check(load().ks_page_plan(_dev(ctx_len, i32, "ctx_len"), _dev(new_len, i32, "new_len"), B,
-                               _dev(free_pages, i32, "free_pages"), n_free, n_pages, page_size,
-                               _dev(block_table, i32, "block_table"), block_table.shape[1], cap,
-                               _dev(cu_new, i32, "cu_new"), _dev(kv_len, i32, "kv_len"),
-                               _dev(positions, i32, "positions"), _dev(slots, i32, "slots"),
-                               _dev(n_taken, i32, "n_taken"), _dev(status, i32, "status"),
-                               _stream()))
+    _same(free_pages, (n_free,), "free_pages")
+    _same(positions, (cap,), "positions")
+    _same(slots, (cap,), "slots")
+    d = _device(ctx_len)
+    _check(load().ks_page_plan(_ptr(ctx_len, _I32, "ctx_len", d), _ptr(new_len, _I32, "new_len", d),
+                               B, _ptr(free_pages, _I32, "free_pages", d), n_free, n_pages,
+                               page_size, _ptr(block_table, _I32, "block_table", d),
+                               block_table.shape[1], cap, _ptr(cu_new, _I32, "cu_new", d),
+                               _ptr(kv_len, _I32, "kv_len", d), _ptr(positions, _I32, "positions", d),
+                               _ptr(slots, _I32, "slots", d), _ptr(n_taken, _I32, "n_taken", d),
+                               _status_ptr(status, d), _stream_of(d)))
 
 
-def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor) -> PagePool:
+def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, dev: int) -> PagePool:
     """One layer's pages [n_pages][page_size][Hkv][hd] of K and V."""
-    if k_pages.dim() != 4:
-        raise KnapSpecError("k_pages / v_pages must both be [n_pages][page_size][Hkv][hd]")
-    n_pages, page_size, Hkv, hd = k_pages.shape
-    _shape(v_pages, (n_pages, page_size, Hkv, hd), "v_pages")
-    return PagePool(_dev(k_pages, torch.bfloat16, "k_pages"), _dev(v_pages, torch.bfloat16, "v_pages"),
-                    n_pages, page_size, Hkv, hd)
+    return PagePool(_ptr(k_pages, _BF16, "k_pages", dev), _ptr(v_pages, _BF16, "v_pages", dev),
+                    *k_pages.shape)
 
 
-def _token_stride(t: torch.Tensor, shape: Sequence[int], name: str) -> int:
+def _token_stride(t: torch.Tensor, shape: tuple, name: str) -> int:
     """Row stride of [tokens][heads][hd] rows whose heads lie side by side (a
     slice of a fused projection's output will do)."""
-    _shape(t, shape, name)
+    _same(t, shape, name)
     n, H, hd = shape
     if t.is_contiguous():
         return H * hd
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != hd):
-        raise KnapSpecError(f"{name}: a token's heads must lie side by side, "
-                            f"got strides {tuple(t.stride())}")
-    return t.stride(0) if n > 1 else H * hd
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != hd):
+        raise KnapSpecError(f"{name}: a token's heads must lie side by side, got strides {st}")
+    return st[0] if n > 1 else H * hd
 
 
-def _strided_dev(t: Optional[torch.Tensor], name: str) -> Optional[int]:
-    """_dev for bf16 rows that _token_stride has accepted."""
+def _strided_ptr(t: Optional[torch.Tensor], name: str, dev: int) -> Optional[int]:
+    """_ptr for bf16 rows that _token_stride has accepted."""
     if t is None:
         return None
-    _dev(t[:0], torch.bfloat16, name)          # device and dtype
+    if t.get_device() != dev or t.dtype is not _BF16:
+        _dev(t[:0], _BF16, name)               # raises
     return t.data_ptr()
 
 
@@ -455,9 +490,13 @@ def rope_append_bf16(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor
     if k.dim() != 3:
         raise KnapSpecError(f"k must be [n][Hkv][hd], got {tuple(k.shape)}")
     n, Hkv, hd = k.shape
-    _shape(k_pages, tuple(k_pages.shape[:2]) + (Hkv, hd), "k_pages")
+    if k_pages.dim() != 4 or k_pages.shape[2:] != (Hkv, hd):
+        raise KnapSpecError(f"k_pages must be [n_pages][page_size][{Hkv}][{hd}], "
+                            f"got {tuple(k_pages.shape)}")
+    _same(v_pages, k_pages.shape, "v_pages")
     for t, name in ((positions, "positions"), (slots, "slots")):
-        _rows(t, n, (), name)
+        if t.dim() != 1 or t.shape[0] < n:
+            raise KnapSpecError(f"{name} must hold {n} entries, got {tuple(t.shape)}")
     if (q is None) != (q_out is None):
         raise KnapSpecError("q and q_out go together")
     Hq, qs = 1, 0
@@ -466,19 +505,17 @@ def rope_append_bf16(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor
             raise KnapSpecError(f"q must be [n][Hq][hd], got {tuple(q.shape)}")
         Hq = q.shape[1]
         qs = _token_stride(q, (n, Hq, hd), "q")
-        _shape(q_out, (n, Hq, hd), "q_out")
+        _same(q_out, (n, Hq, hd), "q_out")
     ks = _token_stride(k, (n, Hkv, hd), "k")
     vs = _token_stride(v, (n, Hkv, hd), "v")
-    _shape(v_pages, tuple(k_pages.shape), "v_pages")
-    if status is not None and status.numel() < 1:
-        raise KnapSpecError("status must hold one int32")
-    pool = _pool(k_pages, v_pages)
-    _check(load().ks_rope_append_bf16(_strided_dev(q, "q"), qs, _strided_dev(k, "k"), ks,
-                                      _strided_dev(v, "v"), vs, n, Hq, ctypes.byref(pool),
-                                      _dev(positions, torch.int32, "positions"),
-                                      _dev(slots, torch.int32, "slots"), rope_base,
-                                      _dev(q_out, torch.bfloat16, "q_out"),
-                                      _dev(status, torch.int32, "status"), _stream()))
+    d = _device(k)
+    _check(load().ks_rope_append_bf16(_strided_ptr(q, "q", d), qs, _strided_ptr(k, "k", d), ks,
+                                      _strided_ptr(v, "v", d), vs, n, Hq,
+                                      ctypes.byref(_pool(k_pages, v_pages, d)),
+                                      _ptr(positions, _I32, "positions", d),
+                                      _ptr(slots, _I32, "slots", d), rope_base,
+                                      None if q_out is None else _ptr(q_out, _BF16, "q_out", d),
+                                      _status_ptr(status, d), _stream_of(d)))
 
 
 def paged_attention_workspace_size() -> int:
@@ -503,21 +540,23 @@ def paged_attention_bf16(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     if q.dim() != 3:
         raise KnapSpecError(f"q must be [n][Hq][hd], got {tuple(q.shape)}")
     n, Hq, hd = q.shape
-    _shape(out, (n, Hq, hd), "out")
-    _shape(k_pages, tuple(k_pages.shape[:3]) + (hd,), "k_pages")
+    _same(out, q.shape, "out")
+    if k_pages.dim() != 4 or k_pages.shape[3] != hd:
+        raise KnapSpecError(f"k_pages must be [n_pages][page_size][Hkv][{hd}], "
+                            f"got {tuple(k_pages.shape)}")
+    _same(v_pages, k_pages.shape, "v_pages")
     if block_table.dim() != 2:
         raise KnapSpecError(f"block_table must be [B][max_blocks], got {tuple(block_table.shape)}")
     B, max_blocks = block_table.shape
-    _shape(cu_new, (B + 1,), "cu_new")
-    _shape(kv_len, (B,), "kv_len")
-    if status is not None and status.numel() < 1:
-        raise KnapSpecError("status must hold one int32")
-    pool = _pool(k_pages, v_pages)
+    _same(cu_new, (B + 1,), "cu_new")
+    _same(kv_len, (B,), "kv_len")
+    d = _device(q)
     _check(load().ks_paged_attention_bf16(
-        _dev(q, torch.bfloat16, "q"), ctypes.byref(pool), _dev(block_table, torch.int32, "block_table"),
-        max_blocks, _dev(cu_new, torch.int32, "cu_new"), _dev(kv_len, torch.int32, "kv_len"), B, n,
-        max_new, Hq, window, sinks, _dev(out, torch.bfloat16, "out"), _dev(ws, name="workspace"),
-        ws.numel() * ws.element_size(), _dev(status, torch.int32, "status"), _stream()))
+        _ptr(q, _BF16, "q", d), ctypes.byref(_pool(k_pages, v_pages, d)),
+        _ptr(block_table, _I32, "block_table", d), max_blocks, _ptr(cu_new, _I32, "cu_new", d),
+        _ptr(kv_len, _I32, "kv_len", d), B, n, max_new, Hq, window, sinks, _ptr(out, _BF16, "out", d),
+        _ptr(ws, ws.dtype, "workspace", d), ws.numel() * ws.element_size(), _status_ptr(status, d),
+        _stream_of(d)))
 
 
 def check_bounded_wait(limit_us: int, status: torch.Tensor,

@@ -95,6 +95,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
 
   if (threadIdx.x == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(smem_u32(&tail->sched.full[s]), 1);
       mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // V, S, P.V and 8 softmax warps
@@ -155,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const bool mine = (lane & 15) < kBlock / p.box && (lane >> 4) < C::PANELS;
       const uint32_t box_off = sbase + off + (lane >> 4) * C::KV_PANEL + (lane & 15) * p.box * 128;
-      if (lane == 0) prefetch_tmap(tm);
       while (ok) {
         const Seg* s = is_k ? walk.next(p, tail->sched, abort) : rd.peek(p, tail->sched, abort);
         if (!s || s->nb == 0) break;
@@ -191,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kph = 0;
       bool ok = true;
       const int box_rows = p.grp * p.tile_tokens;
-      if (lane == 0) prefetch_tmap(&tmQ);
       const uint64_t dq0 = desc_kmajor_sw128(sbase);
       const uint64_t dk0 = desc_kmajor_sw128(sbase + C::OFF_K);
       while (ok) {
@@ -472,12 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (r < rows) __stcg(reinterpret_cast<float2*>(pc) + r, make_float2(m_new * sl2, sum));
-      __threadfence();
       if (!meet()) break;
       if (q4 == 0 && lane == 0) tail->last[G] = arrive_piece(p, s);
       if (!meet()) break;
       if (tail->last[G]) {
-        __threadfence();
         join_pieces<HD>(p, s, q4, 4, lane);
       }
       rd.release(tail->sched);

@@ -52,12 +52,13 @@ struct Tail {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];   // by block parity
-  uint64_t o_free;                                        // one phase per piece
+  uint64_t o_free[2];                                     // by piece parity
   uint64_t esync, drain[2];                               // meetings of all softmax warps; MMA drains
   uint32_t tmem_base;
   int abort, last;
-  alignas(16) float nref[128], alpha[128];                // -reference and rescale factor by row
-  float wmax[4][128], lsum[4][128];                       // by warp and row
+  alignas(16) float nref[64], alpha[64];                  // -reference and rescale factor by row
+  float wmax[4][64];                                      // by warp and row
+  float lsum[2][4][64], ref[2][64], inv[64];              // a finished piece's, by its parity
 };
 constexpr int kTailBytes = (int)((sizeof(Tail) + 255) / 256 * 256);
 
@@ -130,6 +131,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
 
   if (threadIdx.x == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
     for (int s = 0; s < kMaxRing; ++s) {
       mbar_init(smem_u32(&tail->k_full[s]), 1);
       mbar_init(smem_u32(&tail->k_empty[s]), 1);
@@ -147,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&tail->s_free[b]), 8);
       mbar_init(smem_u32(&tail->p_full[b]), 8);
       mbar_init(smem_u32(&tail->pv_done[b]), 1);
+      mbar_init(smem_u32(&tail->o_free[b]), 8);
     }
-    mbar_init(smem_u32(&tail->o_free), 8);
     mbar_init(smem_u32(&tail->esync), 8);
     mbar_init(smem_u32(&tail->drain[0]), 1);
     mbar_init(smem_u32(&tail->drain[1]), 1);
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tail->tmem_base;
-  constexpr uint32_t kS = 0, kO = 256;         // TMEM columns: S[b] at 128 b, then O
+  constexpr uint32_t kS = 0, kO = 256;         // TMEM columns: S[b] at 128 b, O[piece parity] from 256
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ TMA: the walk, Q and K; V
@@ -189,10 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const bool mine = (lane & 15) < kBlock / p.box && (lane >> 4) < PANELS;
     const uint32_t box_off = base + (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
-    if (lane == 0) {
-      prefetch_tmap(tm);
-      if (is_k) prefetch_tmap(&tmQ);
-    }
     while (ok) {
       const Seg* s = is_k ? walk.next(p, tail->sched, abort) : rd.peek(p, tail->sched, abort);
       if (!s || s->nb == 0) break;
@@ -295,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rp16 = row_panel >> 4;
     while (ok) {
       if (!rd.take(p, tail->sched, abort, s) || s.nb == 0) break;
-      // O still holds the piece before this one until its rows have been read
-      if (n_seg > 0 && !KS_PAGED_WAIT(tail->o_free, (n_seg - 1) & 1)) break;
+      // O holds the piece before the last until its rows have been read
+      const uint32_t ob = n_seg & 1;
+      if (n_seg >= 2 && !KS_PAGED_WAIT(tail->o_free[ob], ((n_seg - 2) >> 1) & 1)) break;
       ++n_seg;
       for (int e = 0; e < s.nb; ++e, ++i) {
         const uint32_t b = i & 1;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t dp = dp0 + (uint64_t)((b * p_tile) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kBlock / 16; ++kk)
-            mma_bf16(tmem + kO, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
+            mma_bf16(tmem + kO + ob * 64, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
                      dp + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, e > 0 || kk > 0);
           mma_commit(smem_u32(&tail->v_empty[slot]));
           mma_commit(smem_u32(&tail->pv_done[b]));
@@ -336,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_key = (key >> 6) * row_panel + (key & 7) * 2;
     const uint32_t p_chunk = (key & 63) >> 3;
     SegReader rd;
-    Seg s;
     uint32_t j = 0, esyncs = 0;
     int k_slot = 0;
     bool ok = true;
@@ -368,191 +368,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return true;
     };
-    while (ok) {
-      if (!rd.take(p, tail->sched, abort, s)) break;
-      if (s.nb == 0) {
-        finished = true;
-        break;
+    // A finished piece's output waits until its successor's first block is under way (or the share
+    // is over): the last P.V's latency is hidden, and no product waits for the stores.
+    bool pending = false;
+    uint32_t last_j = 0;                       // number of the pending piece's last block
+    auto finish = [&]() -> bool {
+      const uint32_t pn = rd.n - 2, par = pn & 1;   // rd has gone one piece further
+      const Seg& t = tail->sched.seg[pn % kSegRing];
+      const int rows = t.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
+      const int r0 = G ? half * 8 : 0, nch = G ? chunks - half : half;
+      const bool cut = t.nb < t.blocks;
+      unsigned char* pc = own_piece(p, t);
+      pending = false;
+      if (!meet()) return false;
+      if (key < nch * 8) {
+        const int r = r0 + key;
+        const float sum = (tail->lsum[par][0][r] + tail->lsum[par][1][r]) +
+                          (tail->lsum[par][2][r] + tail->lsum[par][3][r]);
+        tail->inv[r] = sum > 0.f ? 1.0f / sum : 0.f;
+        if (cut) __stcg(reinterpret_cast<float2*>(pc) + r, make_float2(tail->ref[par][r], sum));
       }
-      const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
-      const int r0 = G ? half * 8 : 0;         // this group's first row
-      const int nch = G ? chunks - half : half;
-      float l[CPG];
+      if (!wait_pv(last_j) || !meet()) return false;
+      float* part = reinterpret_cast<float*>(pc + kPieceStats) + r0 * HD + key;
+      int hh = r0 % p.grp;
+      __nv_bfloat16* dst =
+          p.out + ((long long)(t.row0 + r0 / p.grp) * p.Hq + t.g * p.grp + hh) * HD + key;
+      const long long next = (long long)(p.Hq - p.grp + 1) * HD;
 #pragma unroll
-      for (int c = 0; c < CPG; ++c) l[c] = 0.f;
-      for (int i = 0; ok && i < s.nb; ++i, ++j) {
-        const uint32_t b = j & 1;
-        if (!KS_PAGED_WAIT(tail->s_full[b], (j >> 1) & 1)) {
-          ok = false;
-          break;
-        }
-        if (warp == 4 && lane == 0) mbar_arrive(smem_u32(&tail->k_empty[k_slot]));   // K_j read
-        if (++k_slot == p.k_slots) k_slot = 0;
-        tc_fence_after();
-        float sc[CPG];
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-          if (c < nch) tmem_ld8(tmem + lanes + kS + b * 128 + r0 + c * 8, &sc[c * 8]);
+      for (int c = 0; c < NCH; ++c) {
+        if (c >= nch) break;
+        float o[8];
+        tmem_ld8(tmem + lanes + kO + par * 64 + r0 + c * 8, o);
         tmem_wait_ld();
+        reg_fence8(o);
+        if (key < HD)
 #pragma unroll
-        for (int c = 0; c < NCH; ++c) reg_fence8(&sc[c * 8]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[b]));   // S_{j+2} may be computed now
-        if (nch > 0) {
-          const int kb = s.key_block(i);
-          if (s.masked(p, kb)) {
-            // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
-            // on, and while the key is in its window up to row (k - p_first + window) grp
-            const int k = kb * kBlock + key;
-            const long long d = (long long)k - s.p_first;
-            const int from = (int)(d < 0 ? 0 : d > 128 ? 128 : d) * p.grp;
-            int to = 1 << 20;
-            if (p.window > 0 && k >= p.sinks) {
-              const long long e = d + p.window;
-              to = (int)(e < 0 ? 0 : e > 128 ? 128 : e) * p.grp;
-            }
-#pragma unroll
-            for (int c = 0; c < CPG; ++c)
-              if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;
-          }
-          // has a score outgrown its row's reference?
-          bool grow = i == 0;
-          if (i > 0) {
-            bool any = false;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-              if (c < nch) {
-                const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-                const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
-                const float* x = &sc[c * 8];
-                const float m0 = fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
-                const float m1 = fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
-                any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
-              }
-            any = __any_sync(0xffffffffu, any);
-            const int n = vote(any && lane == 0);
-            if (n >= 32) {
-              ok = false;
-              break;
-            }
-            grow = n > 0;
-          }
-          if (grow) {
-            // maxima over the keys, and the rows' new references
-#pragma unroll
-            for (int c0 = 0; c0 < CPG; c0 += 32) {
-              float m = 0.f;
-#pragma unroll
-              for (int c = c0; c < c0 + 32 && c < CPG; ++c)
-                if (c < nch * 8) {
-                  const float w = warp_max(sc[c]);
-                  if (lane == c - c0) m = w;
-                }
-              if (c0 + lane < nch * 8) tail->wmax[q4][r0 + c0 + lane] = m;
-            }
-            if (!meet()) {
-              ok = false;
-              break;
-            }
-            if (key < nch * 8) {
-              const int r = r0 + key;
-              const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
-                                           fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
-              const float old = i == 0 ? kNoRef : -tail->nref[r];
-              const bool up = mx - old > kStale;
-              tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
-              tail->nref[r] = up ? -mx : -old;
-            }
-            if (!meet()) {
-              ok = false;
-              break;
-            }
-            if (i > 0) {
-              // sums and O hold the blocks before relative to the old references
-              if (!wait_pv(j - 1)) {
-                ok = false;
-                break;
-              }
-#pragma unroll
-              for (int c = 0; c < NCH; ++c)
-                if (c < nch) {
-                  float v[8];
-                  const uint32_t to = tmem + lanes + kO + r0 + c * 8;
-                  tmem_ld8(to, v);
-                  tmem_wait_ld();
-                  reg_fence8(v);
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const float a = tail->alpha[r0 + c * 8 + e];
-                    v[e] *= a;
-                    l[c * 8 + e] *= a;
-                  }
-                  tmem_st8(to, v);
-                }
-              tmem_wait_st();
-            }
-          }
-          // the P buffer was last read by PV_{j-2}
-          if (j >= 2 && !wait_pv(j - 2)) {
-            ok = false;
-            break;
-          }
-          unsigned char* pt = smem + off_p + b * p_tile + p_key + r0 * 128;
-#pragma unroll
-          for (int c = 0; c < NCH; ++c)
-            if (c < nch) {
-              const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-              const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
-              const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float w = ex2(fmaf(sc[c * 8 + e], sl2, n[e]));
-                l[c * 8 + e] += w;
-                *reinterpret_cast<__nv_bfloat16*>(pt + (c * 8 + e) * 128 + ((p_chunk ^ e) << 4)) =
-                    __float2bfloat16_rn(w);
-              }
-            }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        } else if (j >= 2 && !wait_pv(j - 2)) {   // keep in step
-          ok = false;
-          break;
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tail->p_full[b]));
-      }
-      if (!ok) break;
-      // -------------------------------------------------------- a piece is done
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-        if (c < nch) {
-          const float w = warp_sum8(&l[c * 8], lane);
-          if ((lane & 3) == 0) tail->lsum[q4][r0 + c * 8 + (lane >> 2)] = w;
-        }
-      if (!wait_pv(j - 1) || !meet()) break;
-      const bool cut = s.nb < s.blocks;
-      float o[CPG];
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-        if (c < nch) tmem_ld8(tmem + lanes + kO + r0 + c * 8, &o[c * 8]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) reg_fence8(&o[c * 8]);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tail->o_free));
-      if (!cut) {
-        int t = r0 / p.grp, hh = r0 - t * p.grp;
-        if (key < HD) {
-          __nv_bfloat16* dst = p.out + ((long long)(s.row0 + t) * p.Hq + s.g * p.grp + hh) * HD + key;
-          const long long next = (long long)(p.Hq - p.grp + 1) * HD;
-#pragma unroll
-          for (int c = 0; c < CPG; ++c)
-            if (c < nch * 8 && r0 + c < rows) {
-              const int r = r0 + c;
-              const float sum = (tail->lsum[0][r] + tail->lsum[1][r]) + (tail->lsum[2][r] + tail->lsum[3][r]);
-              *dst = __float2bfloat16_rn(sum > 0.f ? o[c] / sum : 0.f);
+          for (int e = 0; e < 8; ++e) {
+            if (r0 + c * 8 + e >= rows) break;
+            if (cut) {
+              __stcg(part + (c * 8 + e) * HD, o[e]);
+            } else {
+              *dst = __float2bfloat16_rn(o[e] * tail->inv[r0 + c * 8 + e]);
               if (++hh == p.grp) {
                 hh = 0;
                 dst += next;
@@ -560,30 +416,195 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dst += HD;
               }
             }
-        }
-      } else {
-        unsigned char* pc = own_piece(p, s);
-        if (key < HD) {
-          float* dst = reinterpret_cast<float*>(pc + kPieceStats) + r0 * HD + key;
-#pragma unroll
-          for (int c = 0; c < CPG; ++c)
-            if (c < nch * 8 && r0 + c < rows) __stcg(dst + c * HD, o[c]);
-        }
-        if (key < nch * 8) {
-          const int r = r0 + key;
-          __stcg(reinterpret_cast<float2*>(pc) + r,
-                 make_float2(-tail->nref[r], (tail->lsum[0][r] + tail->lsum[1][r]) +
-                                                 (tail->lsum[2][r] + tail->lsum[3][r])));
-        }
-        __threadfence();
-        if (!meet_all()) break;
-        if (warp == 4 && lane == 0) tail->last = arrive_piece(p, s);
-        if (!meet_all()) break;
-        if (tail->last) {
-          __threadfence();
-          join_pieces<HD>(p, s, warp - 4, 8, lane);
-        }
+          }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->o_free[par]));
+      if (cut) {
+        if (!meet_all()) return false;
+        if (warp == 4 && lane == 0) tail->last = arrive_piece(p, t);
+        if (!meet_all()) return false;
+        if (tail->last) join_pieces<HD>(p, t, warp - 4, 8, lane);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->sched.empty[pn % kSegRing]));
+      return true;
+    };
+    while (ok) {
+      const Seg* cur = rd.peek(p, tail->sched, abort);
+      if (!cur) break;
+      ++rd.n;
+      const Seg& s = *cur;
+      const int nb = s.nb;                     // 0 at the end of the share
+      const uint32_t par = (rd.n - 1) & 1, to_o = tmem + lanes + kO + par * 64;
+      const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
+      const int r0 = G ? half * 8 : 0;         // this group's first row
+      const int nch = G ? chunks - half : half;
+      float l[CPG];
+#pragma unroll
+      for (int c = 0; c < CPG; ++c) l[c] = 0.f;
+      for (int i = 0; i == 0 || i < nb; ++i) {
+        const uint32_t b = j & 1;
+        if (nb > 0) {
+          if (!KS_PAGED_WAIT(tail->s_full[b], (j >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (warp == 4 && lane == 0) mbar_arrive(smem_u32(&tail->k_empty[k_slot]));   // K_j read
+          if (++k_slot == p.k_slots) k_slot = 0;
+          tc_fence_after();
+          float sc[CPG];
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            if (c < nch) tmem_ld8(tmem + lanes + kS + b * 128 + r0 + c * 8, &sc[c * 8]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) reg_fence8(&sc[c * 8]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[b]));   // S_{j+2} may be computed now
+          if (nch > 0) {
+            const int kb = s.key_block(i);
+            if (s.masked(p, kb)) {
+              // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
+              // on, and while the key is in its window up to row (k - p_first + window) grp
+              const int k = kb * kBlock + key;
+              const long long d = (long long)k - s.p_first;
+              const int from = (int)(d < 0 ? 0 : d > 128 ? 128 : d) * p.grp;
+              int to = 1 << 20;
+              if (p.window > 0 && k >= p.sinks) {
+                const long long e = d + p.window;
+                to = (int)(e < 0 ? 0 : e > 128 ? 128 : e) * p.grp;
+              }
+#pragma unroll
+              for (int c = 0; c < CPG; ++c)
+                if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;
+            }
+            // has a score outgrown its row's reference?
+            bool grow = i == 0;
+            if (i > 0) {
+              bool any = false;
+#pragma unroll
+              for (int c = 0; c < NCH; ++c)
+                if (c < nch) {
+                  const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+                  const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+                  const float* x = &sc[c * 8];
+                  const float m0 = fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
+                  const float m1 = fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
+                  any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
+                }
+              any = __any_sync(0xffffffffu, any);
+              const int n = vote(any && lane == 0);
+              if (n >= 32) {
+                ok = false;
+                break;
+              }
+              grow = n > 0;
+            }
+            if (grow) {
+              // maxima over the keys, and the rows' new references
+#pragma unroll
+              for (int c0 = 0; c0 < CPG; c0 += 32) {
+                float m = 0.f;
+#pragma unroll
+                for (int c = c0; c < c0 + 32 && c < CPG; ++c)
+                  if (c < nch * 8) {
+                    const float w = warp_max(sc[c]);
+                    if (lane == c - c0) m = w;
+                  }
+                if (c0 + lane < nch * 8) tail->wmax[q4][r0 + c0 + lane] = m;
+              }
+              if (!meet()) {
+                ok = false;
+                break;
+              }
+              if (key < nch * 8) {
+                const int r = r0 + key;
+                const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
+                                             fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
+                const float old = i == 0 ? kNoRef : -tail->nref[r];
+                const bool up = mx - old > kStale;
+                tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
+                tail->nref[r] = up ? -mx : -old;
+              }
+              if (!meet()) {
+                ok = false;
+                break;
+              }
+              if (i > 0) {
+                // sums and O hold the blocks before relative to the old references
+                if (!wait_pv(j - 1)) {
+                  ok = false;
+                  break;
+                }
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+                  if (c < nch) {
+                    float v[8];
+                    const uint32_t to = to_o + r0 + c * 8;
+                    tmem_ld8(to, v);
+                    tmem_wait_ld();
+                    reg_fence8(v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                      const float a = tail->alpha[r0 + c * 8 + e];
+                      v[e] *= a;
+                      l[c * 8 + e] *= a;
+                    }
+                    tmem_st8(to, v);
+                  }
+                tmem_wait_st();
+              }
+            }
+            // the P buffer was last read by PV_{j-2}
+            if (j >= 2 && !wait_pv(j - 2)) {
+              ok = false;
+              break;
+            }
+            unsigned char* pt = smem + off_p + b * p_tile + p_key + r0 * 128;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+              if (c < nch) {
+                const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+                const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+                const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float w = ex2(fmaf(sc[c * 8 + e], sl2, n[e]));
+                  l[c * 8 + e] += w;
+                  *reinterpret_cast<__nv_bfloat16*>(pt + (c * 8 + e) * 128 + ((p_chunk ^ e) << 4)) =
+                      __float2bfloat16_rn(w);
+                }
+              }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          } else if (j >= 2 && !wait_pv(j - 2)) {   // keep in step
+            ok = false;
+            break;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&tail->p_full[b]));
+          ++j;
+        }
+        if (pending && !(ok = finish())) break;
+      }
+      if (!ok) break;
+      if (nb == 0) {
+        finished = true;
+        break;
+      }
+      // the piece's sums and references, for finish()
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        if (c < nch) {
+          const float w = warp_sum8(&l[c * 8], lane);
+          if ((lane & 3) == 0) tail->lsum[par][q4][r0 + c * 8 + (lane >> 2)] = w;
+        }
+      if (key < nch * 8) tail->ref[par][r0 + key] = -tail->nref[r0 + key];
+      pending = true;
+      last_j = j - 1;
     }
     if (!voted_out) vote(!finished);
   }

@@ -425,9 +425,9 @@ __device__ __forceinline__ unsigned char* own_piece(const Params& p, const Seg& 
   return piece(p, blockIdx.x, s.k0 == 0);
 }
 
-// One thread, after every writer of the piece has made it visible and the
-// CTA's writers have met: true for the unit's last arrival.  The counter is
-// zero again afterwards.
+// One thread, after the CTA's writers of the piece have met (its fence then covers
+// their stores too): true for the unit's last arrival.  The counter is zero again
+// afterwards.  The readers of the pieces meet it again before they read.
 __device__ __forceinline__ bool arrive_piece(const Params& p, const Seg& s) {
   int* counter = reinterpret_cast<int*>(p.ws) + s.first_cta;
   __threadfence();
@@ -439,59 +439,98 @@ __device__ __forceinline__ bool arrive_piece(const Params& p, const Seg& s) {
   return last;
 }
 
-// Joins a unit's pieces, one row per warp and turn: with M the largest
-// reference, out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, pieces in order.
+// Joins a unit's pieces: with M the largest reference of a row,
+//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, pieces in order.
+// Nothing here depends on bytes, only on how many loads a warp keeps in flight: few rows go one
+// to a warp with 8 pieces at a time (19 pieces of 4 rows: 12 us one piece at a time), many rows 8
+// to a warp (2 pieces of 128 rows: 60 us one row at a time).
+constexpr int kJoinBatch = 8;
+
+template <int HD>
+__device__ __forceinline__ void store_row(const Params& p, const Seg& s, int r, int lane,
+                                          const float* acc, float f) {
+  constexpr int E = HD / 32;
+  const int t = r / p.grp;
+  __nv_bfloat16* dst =
+      p.out + ((long long)(s.row0 + t) * p.Hq + s.g * p.grp + (r - t * p.grp)) * HD + lane * E;
+  uint32_t o[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) o[e] = pack2(acc[2 * e] * f, acc[2 * e + 1] * f);
+  if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[E / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(dst) = o[0];
+}
+
 template <int HD>
 __device__ __forceinline__ void join_pieces(const Params& p, const Seg& s, int warp, int n_warps,
                                             int lane) {
-  constexpr int E = HD / 32;
-  const int rows = s.tokens * p.grp;
-  for (int r = warp; r < rows; r += n_warps) {
-    float M = kNoRef, L = 0.f, acc[E] = {};
-    for (int i0 = 0; i0 < s.pieces; i0 += 32)
-      if (i0 + lane < s.pieces)
-        M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(
-                                piece(p, s.first_cta + i0 + lane, i0 + lane == 0)) + r).x);
+  constexpr int E = HD / 32, NB = kJoinBatch;
+  const int rows = s.tokens * p.grp, n = s.pieces;
+  const size_t next = 2 * kPieceBytes;         // from a piece to the unit's next one, after the first
+  const unsigned char* first = piece(p, s.first_cta, 1);
+  const unsigned char* rest = piece(p, s.first_cta, 0);   // + i * next, i >= 1
+  auto stats = [&](int i, int r) {
+    return __ldcg(reinterpret_cast<const float2*>(i ? rest + i * next : first) + r);
+  };
+  auto load = [&](int i, int r, float* v) {
+    const float* src =
+        reinterpret_cast<const float*>((i ? rest + i * next : first) + kPieceStats) + r * HD + lane * E;
+    if (E == 4) *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
+    else *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
+  };
+  alignas(16) float v[NB][E];
+  if (rows <= 2 * n_warps) {
+    for (int r = warp; r < rows; r += n_warps) {
+      float M = kNoRef, L = 0.f, acc[E] = {};
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, stats(i, r).x);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    for (int i0 = 0; i0 < s.pieces; i0 += 32) {
-      float w = 0.f, wl = 0.f;
-      if (i0 + lane < s.pieces) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(
-                                     piece(p, s.first_cta + i0 + lane, i0 + lane == 0)) + r);
-        w = ex2(ml.x - M);
-        wl = w * ml.y;
-      }
-      const int n = min(32, s.pieces - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float* o = reinterpret_cast<const float*>(
-                             piece(p, s.first_cta + i0 + i, i0 + i == 0) + kPieceStats) +
-                         r * HD + lane * E;
-        const float ws = __shfl_sync(0xffffffffu, w, i);
-        L += __shfl_sync(0xffffffffu, wl, i);
-        if (E == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
-          acc[0] += ws * v.x;
-          acc[1] += ws * v.y;
-          acc[E - 2] += ws * v.z;
-          acc[E - 1] += ws * v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
-          acc[0] += ws * v.x;
-          acc[1] += ws * v.y;
+      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += NB) {
+        const bool on = lane < NB && i0 + lane < n;
+        const float2 ml = stats(min(i0 + (lane & (NB - 1)), n - 1), r);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) load(min(i0 + k, n - 1), r, v[k]);
+        const float w = on ? ex2(ml.x - M) : 0.f, wl = w * ml.y;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          L += __shfl_sync(0xffffffffu, wl, k);
+          if (i0 + k < n)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += wk * v[k][e];
         }
+      }
+      store_row<HD>(p, s, r, lane, acc, L > 0.f ? 1.0f / L : 0.f);
+    }
+    return;
+  }
+  for (int r0 = warp * NB; r0 < rows; r0 += n_warps * NB) {
+    // lane l: row r0 + l % 8 of pieces l / 8, l / 8 + 4, ...
+    const int row = min(r0 + (lane & (NB - 1)), rows - 1);
+    float M = kNoRef, L = 0.f, acc[NB][E] = {};
+    for (int i = lane >> 3; i < n; i += 4) M = fmaxf(M, stats(i, row).x);
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = stats(i, row);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) load(i, min(r0 + k, rows - 1), v[k]);
+      const float w = ex2(ml.x - M);
+      L += w * ml.y;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[k][e] += wk * v[k][e];
       }
     }
     const float inv = L > 0.f ? 1.0f / L : 0.f;
-    const int t = r / p.grp;
-    __nv_bfloat16* dst =
-        p.out + ((long long)(s.row0 + t) * p.Hq + s.g * p.grp + (r - t * p.grp)) * HD + lane * E;
-    uint32_t o[E / 2];
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) o[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[E / 2 - 1]);
-    else *reinterpret_cast<uint32_t*>(dst) = o[0];
+    for (int k = 0; k < NB; ++k) {
+      const float f = __shfl_sync(0xffffffffu, inv, k);
+      if (r0 + k < rows) store_row<HD>(p, s, r0 + k, lane, acc[k], f);
+    }
   }
 }
 
