@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < HD / 16; ++kk)
             mma_bf16(tmem + kS + b * 128, dk + (uint64_t)((kk / 4) * ((kBlock * 128) >> 4) + 2 * (kk % 4)),
                      dq + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, kk > 0);
-          // one commit: the softmax warp that sees S_i complete frees K_i's slot
           mma_commit(smem_u32(&tail->s_full[b]));
+          mma_commit(smem_u32(&tail->k_empty[slot]));
           if (e == nb - 1) mma_commit(smem_u32(&tail->q_empty[qb]));
         }
         __syncwarp();
@@ -338,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_chunk = (key & 63) >> 3;
     SegReader rd;
     uint32_t j = 0, esyncs = 0;
-    int k_slot = 0;
     bool ok = true;
     // The group's four warps meet at a hardware barrier (a tenth of an mbarrier's latency) and
     // vote: the count is 0, 1 .. 4 when some of them ask for new references, 32 or more when one
@@ -451,8 +450,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (warp == 4 && lane == 0) mbar_arrive(smem_u32(&tail->k_empty[k_slot]));   // K_j read
-          if (++k_slot == p.k_slots) k_slot = 0;
           tc_fence_after();
           float sc[CPG];
 #pragma unroll
