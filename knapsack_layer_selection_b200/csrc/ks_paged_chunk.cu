@@ -37,6 +37,8 @@ using namespace paged;
 
 namespace {
 
+constexpr float kStale = 8.0f;                 // a new reference once the maximum grows by > 2^8
+
 struct Tail {
   SchedSmem sched;
   uint64_t q_full, q_empty;                                // one phase per piece
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < s.nb; ++e, ++i) {
           const int vs = i % C::VST, kb = s.key_block(e);
           if (!(ok = KS_PAGED_WAIT(tail->v_full[vs], (i / C::VST) & 1))) break;
-          if (s.ragged(kb)) zero_unseen<C::PANELS>(s, kb, smem + C::OFF_V + vs * C::V_SLOT, lane);
+          if (s.ragged(kb)) zero_unseen<C::PANELS>(p, s, kb, smem + C::OFF_V + vs * C::V_SLOT, lane);
           if (!(ok = KS_PAGED_WAIT(tail->p_full, i & 1))) break;
           tc_fence_after();
           if (lane == 0) {

@@ -26,10 +26,10 @@
 //                piece's tail runs beside its successor's first products;
 //   warps 4-11 -- two softmax groups, each half of the query rows (TMEM columns),
 //                thread = key.  P goes to shared memory (two buffers).
-// The softmax reference of a row is kept until a score exceeds it by 2^8, so a
+// The softmax reference of a row is kept until a score exceeds it by 2^24, so a
 // block needs no maximum: each thread only compares, one vote of the group finds
-// the rare block that moves a reference (and always a piece's first), and only
-// then are maxima taken over the keys and O rescaled.  Row sums stay with the
+// the rare block that moves a reference, and only then are maxima taken over the
+// keys and O rescaled; a piece begins with the largest score of four keys.  Row sums stay with the
 // keys' threads in fp32 and are added up once per piece; P is rounded to bf16 for
 // the tensor core, O is fp32.
 #include <algorithm>
@@ -43,6 +43,9 @@ using namespace paged;
 
 namespace {
 
+// references move once a score exceeds them by 2^24: P and its sums have fp32's and bf16's range to
+// grow in, and lose no precision by it
+constexpr float kStale = 24.0f;
 constexpr int kMaxRing = 6;                    // slots of the K ring, and of the V ring
 constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 118784;             // one CTA holds an SM and its 512 TMEM columns
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = i & 1;
         const int kb = s.key_block(e);
         if (!(ok = KS_PAGED_WAIT(tail->v_full[slot], phase))) break;
-        if (s.ragged(kb)) zero_unseen<PANELS>(s, kb, smem + off_v + slot * SLOT, lane);
+        if (s.ragged(kb)) zero_unseen<PANELS>(p, s, kb, smem + off_v + slot * SLOT, lane);
         if (!(ok = KS_PAGED_WAIT(tail->p_full[b], (i >> 1) & 1))) break;
         tc_fence_after();
         if (lane == 0) {
@@ -478,28 +481,54 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < CPG; ++c)
                 if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;
             }
-            // has a score outgrown its row's reference?
-            bool grow = i == 0;
-            if (i > 0) {
-              bool any = false;
+            if (i == 0) {
+              // a piece's first references: the largest score of four of its keys will do, since
+              // a row's P and sums may grow to 2^kStale times the reference's before it moves
+              if (lane == 0) {
 #pragma unroll
-              for (int c = 0; c < NCH; ++c)
-                if (c < nch) {
-                  const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-                  const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
-                  const float* x = &sc[c * 8];
-                  const float m0 = fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
-                  const float m1 = fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
-                  any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
-                }
-              any = __any_sync(0xffffffffu, any);
-              const int n = vote(any && lane == 0);
-              if (n >= 32) {
+                for (int c = 0; c < NCH; ++c)
+                  if (c < nch)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4)
+                      *reinterpret_cast<float4*>(&tail->wmax[q4][r0 + c * 8 + e]) = make_float4(
+                          sc[c * 8 + e], sc[c * 8 + e + 1], sc[c * 8 + e + 2], sc[c * 8 + e + 3]);
+              }
+              if (!meet()) {
                 ok = false;
                 break;
               }
-              grow = n > 0;
+              if (key < nch * 8) {
+                const int r = r0 + key;
+                const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
+                                             fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
+                tail->nref[r] = -fmaxf(mx, kNoRef);
+              }
+              if (!meet()) {
+                ok = false;
+                break;
+              }
             }
+            // has a score outgrown its row's reference?
+            bool any = false;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+              if (c < nch) {
+                const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+                const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+                const float* x = &sc[c * 8];
+                const float m0 =
+                    fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
+                const float m1 =
+                    fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
+                any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
+              }
+            any = __any_sync(0xffffffffu, any);
+            const int votes = vote(any && lane == 0);
+            if (votes >= 32) {
+              ok = false;
+              break;
+            }
+            const bool grow = votes > 0;
             if (grow) {
               // maxima over the keys, and the rows' new references
 #pragma unroll
@@ -521,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = r0 + key;
                 const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
                                              fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
-                const float old = i == 0 ? kNoRef : -tail->nref[r];
+                const float old = -tail->nref[r];
                 const bool up = mx - old > kStale;
                 tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
                 tail->nref[r] = up ? -mx : -old;

@@ -30,7 +30,6 @@ constexpr int kTileRows = 128;               // query rows of a tile, at most
 constexpr int kThreads = 384;                // both kernels: 12 warps
 constexpr int kWarps = kThreads / 32;
 constexpr float kNoRef = -1e30f;             // reference of a row that has seen no key
-constexpr float kStale = 8.0f;               // a new reference once the maximum grows by > 2^8
 
 // Workspace: one arrival counter per CTA (of the unit whose first piece it
 // holds), then two pieces per CTA: reference and sum of 128 rows, and the rows.
@@ -119,7 +118,6 @@ struct alignas(16) Seg {
   __device__ __forceinline__ bool unseen(int j0, int j1) const {
     return j0 > p_last || (j1 < lo && j0 >= sinks);
   }
-  __device__ __forceinline__ bool sees(int j) const { return j <= p_last && (j >= lo || j < sinks); }
   // Some key of this block is hidden from some token.
   __device__ __forceinline__ bool masked(const Params& p, int kb) const {
     const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
@@ -404,15 +402,28 @@ struct BoxRow {
 };
 
 // Zeroes the rows of a V block that no token of the tile sees (their weights are
-// zero, but zero times what the page holds there need not be); one warp.
+// zero, but zero times what the page holds there need not be); one warp.  Boxes of
+// which nothing is seen hold zeros already, so what is left lies behind the last
+// seen key in its box, and at either end of the gap between sinks and window.
 template <int PANELS>
-__device__ __forceinline__ void zero_unseen(const Seg& s, int kb, unsigned char* v, int lane) {
-  for (int r = lane >> 3; r < kBlock; r += 4)
-    if (!s.sees(kb * kBlock + r))
+__device__ __forceinline__ void zero_rows(unsigned char* v, int from, int to, int lane) {
+  for (int r = from + (lane >> 3); r < to; r += 4)
 #pragma unroll
-      for (int pn = 0; pn < PANELS; ++pn)
-        *reinterpret_cast<uint4*>(v + pn * kBlock * 128 + r * 128 + (lane & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+    for (int pn = 0; pn < PANELS; ++pn)
+      *reinterpret_cast<uint4*>(v + pn * kBlock * 128 + r * 128 + (lane & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+}
+template <int PANELS>
+__device__ __forceinline__ void zero_unseen(const Params& p, const Seg& s, int kb, unsigned char* v,
+                                            int lane) {
+  const int j0 = kb * kBlock, up = p.box - 1;
+  const int tail = max(0, min(kBlock, s.p_last + 1 - j0));
+  zero_rows<PANELS>(v, tail, min(kBlock, (tail + up) & ~up), lane);
+  const int g0 = max(0, min(kBlock, s.sinks - j0)), g1 = max(0, min(kBlock, s.lo - j0));
+  if (g0 < g1) {                               // the gap [g0, g1)
+    zero_rows<PANELS>(v, g0, min(g1, (g0 + up) & ~up), lane);
+    zero_rows<PANELS>(v, max(g0, g1 & ~up), g1, lane);
+  }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
 }
