@@ -37,6 +37,7 @@ using namespace paged;
 
 namespace {
 
+constexpr int kThreads = 384;
 constexpr float kStale = 8.0f;                 // a new reference once the maximum grows by > 2^8
 
 struct Tail {
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ones[e] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // visible to the tensor core
-  locate(p, tail->sched);
+  locate<kThreads / 32>(p, tail->sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -146,46 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     regs_dec<C::REGS_LOW>();
     if (warp == 0 || warp == 3) {
-      // ---------------------------------------------------------- TMA: K and the walk, V
+      // ---------------------------------------------------------- TMA: the walk and K; V
       const bool is_k = warp == 0;
-      const CUtensorMap* tm = is_k ? &tmK : &tmV;
-      uint64_t *full = is_k ? tail->k_full : tail->v_full, *empty = is_k ? tail->k_empty : tail->v_empty;
-      const int nst = is_k ? C::KST : C::VST, stride = is_k ? C::KV_BLOCK : C::V_SLOT;
-      const uint32_t off = is_k ? C::OFF_K : C::OFF_V;
-      Walker walk;
-      SegReader rd;
-      if (is_k) walk.start(p, tail->sched);
-      int n_loads = 0, slot = 0;
-      uint32_t phase = 1;
-      bool ok = true;
-      const bool mine = (lane & 15) < kBlock / p.box && (lane >> 4) < C::PANELS;
-      const uint32_t box_off = sbase + off + (lane >> 4) * C::KV_PANEL + (lane & 15) * p.box * 128;
-      while (ok) {
-        const Seg* s = is_k ? walk.next(p, tail->sched, abort) : rd.peek(p, tail->sched, abort);
-        if (!s || s->nb == 0) break;
-        const int nb = s->nb, x = s->g * HD + (lane >> 4) * 64;
-        BoxRow next;
-        next.fetch(p, *s, s->key_block(0), lane);
-        for (int i = 0; i < nb; ++i) {
-          const BoxRow cur = next;
-          if (i + 1 < nb) next.fetch(p, *s, s->key_block(i + 1), lane);
-          if (!(ok = KS_PAGED_WAIT(empty[slot], phase))) break;
-          const uint32_t fb = smem_u32(&full[slot]);
-          if (lane == 0) mbar_arrive_expect_tx(fb, C::KV_BLOCK);
-          __syncwarp();
-          if (mine) tma_load_2d(box_off + slot * stride, tm, x, cur.slot(p), fb);
-          ++n_loads;
-          if (++slot == nst) {
-            slot = 0;
-            phase ^= 1;
-          }
-        }
-        if (!is_k) rd.release(tail->sched);
-      }
-      // drain the copies still in flight before leaving
-      if (lane == 0)
-        for (int i = n_loads > nst ? n_loads - nst : 0; i < n_loads; ++i)
-          mbar_wait_drain(smem_u32(&full[i % nst]), (uint32_t)(i / nst) & 1u, p.status);
+      const Ring ring{is_k ? &tmK : &tmV, is_k ? tail->k_full : tail->v_full,
+                      is_k ? tail->k_empty : tail->v_empty, sbase + (is_k ? C::OFF_K : C::OFF_V),
+                      is_k ? C::KST : C::VST, is_k ? C::KV_BLOCK : C::V_SLOT};
+      load_share<HD>(p, tail->sched, ring, is_k, abort, [](const Seg&) { return true; });
     } else if (warp == 1) {
       // ---------------------------------------------------------- Q loads and S
       SegReader rd;
@@ -341,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[G]));   // S_{i+2} may be computed now
-        const int kb = s.key_block(i - i0);
-        if (s.masked(p, kb)) {
+        if (s.masked(i - i0)) {
+          const int kb = s.key_block(i - i0);
           // a row sees keys up to its position that are in its window or among the first;
           // as ranges of this block: e <= last, and e >= wlo or e < sinks
           const int key0 = kb * C::BN;

@@ -43,6 +43,9 @@ using namespace paged;
 
 namespace {
 
+constexpr int kThreads = 512, kRegs = 128;      // registers a thread at launch
+constexpr int kRegsRoles = 72, kRegsSoftmax = 160, kRegsOutput = 120;   // and after setmaxnreg
+static_assert(kRegsRoles + 2 * kRegsSoftmax + kRegsOutput == 4 * kRegs, "register split");
 // references move once a score exceeds them by 2^24: P and its sums have fp32's and bf16's range to
 // grow in, and lose no precision by it
 constexpr float kStale = 24.0f;
@@ -55,13 +58,13 @@ struct Tail {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];   // by block parity
-  uint64_t o_free[2];                                     // by piece parity
-  uint64_t esync, drain[2];                               // meetings of all softmax warps; MMA drains
+  uint64_t o_full[2], l_full[2], o_free[2];               // by piece parity
+  uint64_t esync, drain[2];                               // meetings of the output warps; MMA drains
   uint32_t tmem_base;
   int abort, last;
   alignas(16) float nref[64], alpha[64];                  // -reference and rescale factor by row
   float wmax[4][64];                                      // by warp and row
-  float lsum[2][4][64], ref[2][64], inv[64];              // a finished piece's, by its parity
+  float lsum[2][4][64], ref[2][64];                       // a finished piece's, by its parity
 };
 constexpr int kTailBytes = (int)((sizeof(Tail) + 255) / 256 * 256);
 
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(smem_u32(&tail->sched.full[s]), 1);
-      mbar_init(smem_u32(&tail->sched.empty[s]), 11);    // V, S, P.V and 8 softmax warps
+      mbar_init(smem_u32(&tail->sched.empty[s]), 15);    // V, S, P.V, 8 softmax and 4 output warps
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tail->q_full[b]), 1);
@@ -154,9 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&tail->s_free[b]), 8);
       mbar_init(smem_u32(&tail->p_full[b]), 8);
       mbar_init(smem_u32(&tail->pv_done[b]), 1);
-      mbar_init(smem_u32(&tail->o_free[b]), 8);
+      mbar_init(smem_u32(&tail->o_full[b]), 1);
+      mbar_init(smem_u32(&tail->l_full[b]), 8);
+      mbar_init(smem_u32(&tail->o_free[b]), 4);
     }
-    mbar_init(smem_u32(&tail->esync), 8);
+    mbar_init(smem_u32(&tail->esync), 4);
     mbar_init(smem_u32(&tail->drain[0]), 1);
     mbar_init(smem_u32(&tail->drain[1]), 1);
     tail->abort = 0;
@@ -174,163 +179,135 @@ __global__ void __launch_bounds__(kThreads, 1)
         make_uint4(0, 0, 0, 0);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  locate(p, tail->sched);
+  locate<kThreads / 32>(p, tail->sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tail->tmem_base;
   constexpr uint32_t kS = 0, kO = 256;         // TMEM columns: S[b] at 128 b, O[piece parity] from 256
 
-  if (warp == 0 || warp == 2) {
-    // ------------------------------------------------------------ TMA: the walk, Q and K; V
-    const bool is_k = warp == 0;
-    const CUtensorMap* tm = is_k ? &tmK : &tmV;
-    uint64_t *full = is_k ? tail->k_full : tail->v_full, *empty = is_k ? tail->k_empty : tail->v_empty;
-    const int nst = is_k ? p.k_slots : p.v_slots;
-    const uint32_t base = sbase + (is_k ? 0 : off_v);
-    Walker walk;
-    SegReader rd;
-    if (is_k) walk.start(p, tail->sched);
-    int n_loads = 0, slot = 0, n_seg = 0;
-    uint32_t phase = 1;
-    bool ok = true;
-    const bool mine = (lane & 15) < kBlock / p.box && (lane >> 4) < PANELS;
-    const uint32_t box_off = base + (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
-    while (ok) {
-      const Seg* s = is_k ? walk.next(p, tail->sched, abort) : rd.peek(p, tail->sched, abort);
-      if (!s || s->nb == 0) break;
-      const int nb = s->nb, x = s->g * HD + (lane >> 4) * 64;
-      BoxRow next;
-      next.fetch(p, *s, s->key_block(0), lane);
-      if (is_k) {
+  if (warp < 4) {
+    regs_dec<kRegsRoles>();
+    if (warp == 0 || warp == 2) {
+      // ---------------------------------------------------------- TMA: the walk, Q and K; V
+      const bool is_k = warp == 0;
+      const Ring ring{is_k ? &tmK : &tmV, is_k ? tail->k_full : tail->v_full,
+                      is_k ? tail->k_empty : tail->v_empty, sbase + (is_k ? 0 : off_v),
+                      is_k ? p.k_slots : p.v_slots, SLOT};
+      int n_seg = 0;
+      load_share<HD>(p, tail->sched, ring, is_k, abort, [&](const Seg& s) -> bool {
         const int qb = n_seg & 1;
-        if (!(ok = KS_PAGED_WAIT(tail->q_empty[qb], ((n_seg >> 1) & 1) ^ 1))) break;
+        if (!KS_PAGED_WAIT(tail->q_empty[qb], ((n_seg >> 1) & 1) ^ 1)) return false;
         if (lane == 0) {
           const uint32_t qf = smem_u32(&tail->q_full[qb]);
           mbar_arrive_expect_tx(qf, PANELS * box_rows * 128);
           for (int pn = 0; pn < PANELS; ++pn)
-            tma_load_3d(sbase + off_q + qb * q_tile + pn * row_panel, &tmQ, pn * 64, s->g * p.grp,
-                        s->row0, qf);
+            tma_load_3d(sbase + off_q + qb * q_tile + pn * row_panel, &tmQ, pn * 64, s.g * p.grp,
+                        s.row0, qf);
         }
         __syncwarp();
         ++n_seg;
-      }
-      for (int i = 0; i < nb; ++i) {
-        const BoxRow cur = next;
-        if (i + 1 < nb) next.fetch(p, *s, s->key_block(i + 1), lane);
-        if (!(ok = KS_PAGED_WAIT(empty[slot], phase))) break;
-        const uint32_t fb = smem_u32(&full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(fb, SLOT);
-        __syncwarp();
-        if (mine) tma_load_2d(box_off + slot * SLOT, tm, x, cur.slot(p), fb);
-        ++n_loads;
-        if (++slot == nst) {
-          slot = 0;
-          phase ^= 1;
-        }
-      }
-      if (!is_k) rd.release(tail->sched);
-    }
-    // drain the copies still in flight before leaving
-    if (lane == 0) {
-      for (int n = n_seg > 2 ? n_seg - 2 : 0; n < n_seg; ++n)
-        mbar_wait_drain(smem_u32(&tail->q_full[n & 1]), (n >> 1) & 1, p.status);
-      for (int n = n_loads > nst ? n_loads - nst : 0; n < n_loads; ++n)
-        mbar_wait_drain(smem_u32(&full[n % nst]), (uint32_t)(n / nst) & 1, p.status);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S_i = K_i Q^T
-    SegReader rd;
-    int slot = 0;
-    uint32_t phase = 0, i = 0, n_seg = 0;
-    bool ok = true;
-    const uint32_t idesc = idesc_bf16_f32(128, N);
-    const uint64_t dk0 = desc_kmajor_sw128(sbase), dq0 = desc_kmajor_sw128(sbase + off_q);
-    const uint32_t rp16 = row_panel >> 4;
-    while (ok) {
-      const Seg* s = rd.peek(p, tail->sched, abort);
-      const int nb = s ? s->nb : 0;
-      if (nb == 0) break;
-      rd.release(tail->sched);
-      const uint32_t qb = n_seg & 1;
-      ok = KS_PAGED_WAIT(tail->q_full[qb], (n_seg >> 1) & 1);
-      ++n_seg;
-      for (int e = 0; ok && e < nb; ++e, ++i) {
-        // into S buffer i % 2, free once the softmax has copied S_{i-2}
-        const uint32_t b = i & 1;
-        if (i >= 2 && !(ok = KS_PAGED_WAIT(tail->s_free[b], ((i - 2) >> 1) & 1))) break;
-        if (!(ok = KS_PAGED_WAIT(tail->k_full[slot], phase))) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dk = dk0 + (uint64_t)((slot * SLOT) >> 4);
-          const uint64_t dq = dq0 + (uint64_t)((qb * q_tile) >> 4);
+        return true;
+      });
+      if (lane == 0)
+        for (int n = n_seg > 2 ? n_seg - 2 : 0; n < n_seg; ++n)
+          mbar_wait_drain(smem_u32(&tail->q_full[n & 1]), (n >> 1) & 1, p.status);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ S_i = K_i Q^T
+      SegReader rd;
+      int slot = 0;
+      uint32_t phase = 0, i = 0, n_seg = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_bf16_f32(128, N);
+      const uint64_t dk0 = desc_kmajor_sw128(sbase), dq0 = desc_kmajor_sw128(sbase + off_q);
+      const uint32_t rp16 = row_panel >> 4;
+      while (ok) {
+        const Seg* s = rd.peek(p, tail->sched, abort);
+        const int nb = s ? s->nb : 0;
+        if (nb == 0) break;
+        rd.release(tail->sched);
+        const uint32_t qb = n_seg & 1;
+        ok = KS_PAGED_WAIT(tail->q_full[qb], (n_seg >> 1) & 1);
+        ++n_seg;
+        for (int e = 0; ok && e < nb; ++e, ++i) {
+          // into S buffer i % 2, free once the softmax has copied S_{i-2}
+          const uint32_t b = i & 1;
+          if (i >= 2 && !(ok = KS_PAGED_WAIT(tail->s_free[b], ((i - 2) >> 1) & 1))) break;
+          if (!(ok = KS_PAGED_WAIT(tail->k_full[slot], phase))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t dk = dk0 + (uint64_t)((slot * SLOT) >> 4);
+            const uint64_t dq = dq0 + (uint64_t)((qb * q_tile) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            mma_bf16(tmem + kS + b * 128, dk + (uint64_t)((kk / 4) * ((kBlock * 128) >> 4) + 2 * (kk % 4)),
-                     dq + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, kk > 0);
-          mma_commit(smem_u32(&tail->s_full[b]));
-          mma_commit(smem_u32(&tail->k_empty[slot]));
-          if (e == nb - 1) mma_commit(smem_u32(&tail->q_empty[qb]));
-        }
-        __syncwarp();
-        if (++slot == p.k_slots) {
-          slot = 0;
-          phase ^= 1;
+            for (int kk = 0; kk < HD / 16; ++kk)
+              mma_bf16(tmem + kS + b * 128, dk + (uint64_t)((kk / 4) * ((kBlock * 128) >> 4) + 2 * (kk % 4)),
+                       dq + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, kk > 0);
+            mma_commit(smem_u32(&tail->s_full[b]));
+            mma_commit(smem_u32(&tail->k_empty[slot]));
+            if (e == nb - 1) mma_commit(smem_u32(&tail->q_empty[qb]));
+          }
+          __syncwarp();
+          if (++slot == p.k_slots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-    }
-    if (lane == 0) {
-      mma_commit(smem_u32(&tail->drain[0]));
-      mbar_wait_drain(smem_u32(&tail->drain[0]), 0, p.status);
-    }
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ O^T += V_i^T P_i
-    SegReader rd;
-    Seg s;
-    int slot = 0;
-    uint32_t phase = 0, i = 0, n_seg = 0;
-    bool ok = true;
-    const uint32_t idesc = idesc_bf16_f32(128, N) | (1u << 15);   // A (V) MN-major
-    const uint64_t dp0 = desc_kmajor_sw128(sbase + off_p);
-    // head_dim 64: rows 64 .. 127 of the product repeat V's columns some keys further on; nobody
-    // reads them
-    const uint64_t dv0 = desc_mnmajor_sw128(sbase + off_v, PANELS == 2 ? kBlock * 128 : 1024);
-    const uint32_t rp16 = row_panel >> 4;
-    while (ok) {
-      if (!rd.take(p, tail->sched, abort, s) || s.nb == 0) break;
-      // O holds the piece before the last until its rows have been read
-      const uint32_t ob = n_seg & 1;
-      if (n_seg >= 2 && !KS_PAGED_WAIT(tail->o_free[ob], ((n_seg - 2) >> 1) & 1)) break;
-      ++n_seg;
-      for (int e = 0; e < s.nb; ++e, ++i) {
-        const uint32_t b = i & 1;
-        const int kb = s.key_block(e);
-        if (!(ok = KS_PAGED_WAIT(tail->v_full[slot], phase))) break;
-        if (s.ragged(kb)) zero_unseen<PANELS>(p, s, kb, smem + off_v + slot * SLOT, lane);
-        if (!(ok = KS_PAGED_WAIT(tail->p_full[b], (i >> 1) & 1))) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dv = dv0 + (uint64_t)((slot * SLOT) >> 4);
-          const uint64_t dp = dp0 + (uint64_t)((b * p_tile) >> 4);
+      if (lane == 0) {
+        mma_commit(smem_u32(&tail->drain[0]));
+        mbar_wait_drain(smem_u32(&tail->drain[0]), 0, p.status);
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ O^T += V_i^T P_i
+      SegReader rd;
+      Seg s;
+      int slot = 0;
+      uint32_t phase = 0, i = 0, n_seg = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_bf16_f32(128, N) | (1u << 15);   // A (V) MN-major
+      const uint64_t dp0 = desc_kmajor_sw128(sbase + off_p);
+      // head_dim 64: rows 64 .. 127 of the product repeat V's columns some keys further on; nobody
+      // reads them
+      const uint64_t dv0 = desc_mnmajor_sw128(sbase + off_v, PANELS == 2 ? kBlock * 128 : 1024);
+      const uint32_t rp16 = row_panel >> 4;
+      while (ok) {
+        if (!rd.take(p, tail->sched, abort, s) || s.nb == 0) break;
+        // O holds the piece before the last until its rows have been read
+        const uint32_t ob = n_seg & 1;
+        if (n_seg >= 2 && !KS_PAGED_WAIT(tail->o_free[ob], ((n_seg - 2) >> 1) & 1)) break;
+        ++n_seg;
+        for (int e = 0; e < s.nb; ++e, ++i) {
+          const uint32_t b = i & 1;
+          const int kb = s.key_block(e);
+          if (!(ok = KS_PAGED_WAIT(tail->v_full[slot], phase))) break;
+          if (s.ragged(kb)) zero_unseen<PANELS>(p, s, kb, smem + off_v + slot * SLOT, lane);
+          if (!(ok = KS_PAGED_WAIT(tail->p_full[b], (i >> 1) & 1))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t dv = dv0 + (uint64_t)((slot * SLOT) >> 4);
+            const uint64_t dp = dp0 + (uint64_t)((b * p_tile) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBlock / 16; ++kk)
-            mma_bf16(tmem + kO + ob * 64, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
-                     dp + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, e > 0 || kk > 0);
-          mma_commit(smem_u32(&tail->v_empty[slot]));
-          mma_commit(smem_u32(&tail->pv_done[b]));
-        }
-        __syncwarp();
-        if (++slot == p.v_slots) {
-          slot = 0;
-          phase ^= 1;
+            for (int kk = 0; kk < kBlock / 16; ++kk)
+              mma_bf16(tmem + kO + ob * 64, dv + (uint64_t)(kk * ((16 * 128) >> 4)),
+                       dp + (uint64_t)((kk / 4) * rp16 + 2 * (kk % 4)), idesc, e > 0 || kk > 0);
+            mma_commit(smem_u32(&tail->v_empty[slot]));
+            mma_commit(smem_u32(&tail->pv_done[b]));
+            if (e == s.nb - 1) mma_commit(smem_u32(&tail->o_full[ob]));
+          }
+          __syncwarp();
+          if (++slot == p.v_slots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
+      if (lane == 0) {
+        mma_commit(smem_u32(&tail->drain[1]));
+        mbar_wait_drain(smem_u32(&tail->drain[1]), 0, p.status);
+      }
     }
-    if (lane == 0) {
-      mma_commit(smem_u32(&tail->drain[1]));
-      mbar_wait_drain(smem_u32(&tail->drain[1]), 0, p.status);
-    }
-  } else {
+  } else if (warp < 12) {
+    regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
     const int G = (warp - 4) >> 2, q4 = warp & 3;
     const int key = q4 * 32 + lane;            // key of the block = TMEM lane
@@ -340,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_key = (key >> 6) * row_panel + (key & 7) * 2;
     const uint32_t p_chunk = (key & 63) >> 3;
     SegReader rd;
-    uint32_t j = 0, esyncs = 0;
+    uint32_t j = 0;
     bool ok = true;
     // The group's four warps meet at a hardware barrier (a tenth of an mbarrier's latency) and
     // vote: the count is 0, 1 .. 4 when some of them ask for new references, 32 or more when one
@@ -358,11 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       return n;
     };
     auto meet = [&]() -> bool { return vote(false) < 32; };
-    auto meet_all = [&]() -> bool {            // all eight
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tail->esync));
-      return KS_PAGED_WAIT(tail->esync, esyncs++ & 1);
-    };
     // PV_q commits to pv_done[q % 2]; whoever waits for it has waited for PV_{q-2} before, and
     // PV_{q+2} needs a P that this warp has not written, so the parity is unambiguous
     auto wait_pv = [&](uint32_t q) -> bool {
@@ -370,47 +342,254 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return true;
     };
-    // A finished piece's output waits until its successor's first block is under way (or the share
-    // is over): the last P.V's latency is hidden, and no product waits for the stores.
-    bool pending = false;
-    uint32_t last_j = 0;                       // number of the pending piece's last block
-    auto finish = [&]() -> bool {
-      const uint32_t pn = rd.n - 2, par = pn & 1;   // rd has gone one piece further
-      const Seg& t = tail->sched.seg[pn % kSegRing];
-      const int rows = t.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
-      const int r0 = G ? half * 8 : 0, nch = G ? chunks - half : half;
-      const bool cut = t.nb < t.blocks;
-      unsigned char* pc = own_piece(p, t);
-      pending = false;
-      if (!meet()) return false;
-      if (key < nch * 8) {
-        const int r = r0 + key;
+    while (ok) {
+      const Seg* cur = rd.peek(p, tail->sched, abort);
+      if (!cur) break;
+      const Seg& s = *cur;
+      const int nb = s.nb;
+      if (nb == 0) {
+        finished = true;
+        break;
+      }
+      const uint32_t par = rd.n & 1, to_o = tmem + lanes + kO + par * 64;
+      const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
+      const int r0 = G ? half * 8 : 0;         // this group's first row
+      const int nch = G ? chunks - half : half;
+      float l[CPG];
+#pragma unroll
+      for (int c = 0; c < CPG; ++c) l[c] = 0.f;
+      for (int i = 0; i < nb; ++i, ++j) {
+        const uint32_t b = j & 1;
+        if (!KS_PAGED_WAIT(tail->s_full[b], (j >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sc[CPG];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          if (c < nch) tmem_ld8(tmem + lanes + kS + b * 128 + r0 + c * 8, &sc[c * 8]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) reg_fence8(&sc[c * 8]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[b]));   // S_{j+2} may be computed now
+        if (nch > 0) {
+          if (s.masked(i)) {
+            // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
+            // on, and while the key is in its window up to row (k - p_first + window) grp
+            const int k = s.key_block(i) * kBlock + key;
+            const long long d = (long long)k - s.p_first;
+            const int from = (int)(d < 0 ? 0 : d > 128 ? 128 : d) * p.grp;
+            int to = 1 << 20;
+            if (p.window > 0 && k >= p.sinks) {
+              const long long e = d + p.window;
+              to = (int)(e < 0 ? 0 : e > 128 ? 128 : e) * p.grp;
+            }
+#pragma unroll
+            for (int c = 0; c < CPG; ++c)
+              if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;
+          }
+          if (i == 0) {
+            // a piece's first references: the largest score of four of its keys will do, since
+            // a row's P and sums may grow to 2^kStale times the reference's before it moves
+            if (lane == 0) {
+#pragma unroll
+              for (int c = 0; c < NCH; ++c)
+                if (c < nch)
+#pragma unroll
+                  for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<float4*>(&tail->wmax[q4][r0 + c * 8 + e]) = make_float4(
+                        sc[c * 8 + e], sc[c * 8 + e + 1], sc[c * 8 + e + 2], sc[c * 8 + e + 3]);
+            }
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+            if (key < nch * 8) {
+              const int r = r0 + key;
+              const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
+                                           fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
+              tail->nref[r] = -fmaxf(mx, kNoRef);
+            }
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+          }
+          // has a score outgrown its row's reference?
+          bool any = false;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            if (c < nch) {
+              const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+              const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+              const float* x = &sc[c * 8];
+              const float m0 =
+                  fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
+              const float m1 =
+                  fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
+              any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
+            }
+          any = __any_sync(0xffffffffu, any);
+          const int votes = vote(any && lane == 0);
+          if (votes >= 32) {
+            ok = false;
+            break;
+          }
+          const bool grow = votes > 0;
+          if (grow) {
+            // maxima over the keys, and the rows' new references
+#pragma unroll
+            for (int c0 = 0; c0 < CPG; c0 += 32) {
+              float m = 0.f;
+#pragma unroll
+              for (int c = c0; c < c0 + 32 && c < CPG; ++c)
+                if (c < nch * 8) {
+                  const float w = warp_max(sc[c]);
+                  if (lane == c - c0) m = w;
+                }
+              if (c0 + lane < nch * 8) tail->wmax[q4][r0 + c0 + lane] = m;
+            }
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+            if (key < nch * 8) {
+              const int r = r0 + key;
+              const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
+                                           fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
+              const float old = -tail->nref[r];
+              const bool up = mx - old > kStale;
+              tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
+              tail->nref[r] = up ? -mx : -old;
+            }
+            if (!meet()) {
+              ok = false;
+              break;
+            }
+            if (i > 0) {
+              // sums and O hold the blocks before relative to the old references
+              if (!wait_pv(j - 1)) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int c = 0; c < NCH; ++c)
+                if (c < nch) {
+                  float v[8];
+                  const uint32_t to = to_o + r0 + c * 8;
+                  tmem_ld8(to, v);
+                  tmem_wait_ld();
+                  reg_fence8(v);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const float a = tail->alpha[r0 + c * 8 + e];
+                    v[e] *= a;
+                    l[c * 8 + e] *= a;
+                  }
+                  tmem_st8(to, v);
+                }
+              tmem_wait_st();
+            }
+          }
+          // the P buffer was last read by PV_{j-2}
+          if (j >= 2 && !wait_pv(j - 2)) {
+            ok = false;
+            break;
+          }
+          unsigned char* pt = smem + off_p + b * p_tile + p_key + r0 * 128;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            if (c < nch) {
+              const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
+              const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+              const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float w = ex2(fmaf(sc[c * 8 + e], sl2, n[e]));
+                l[c * 8 + e] += w;
+                *reinterpret_cast<__nv_bfloat16*>(pt + (c * 8 + e) * 128 + ((p_chunk ^ e) << 4)) =
+                    __float2bfloat16_rn(w);
+              }
+            }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else if (j >= 2 && !wait_pv(j - 2)) {   // keep in step
+          ok = false;
+          break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail->p_full[b]));
+      }
+      if (!ok) break;
+      // the piece's sums and references, for the output warps
+      if (rd.n >= 2 && !KS_PAGED_WAIT(tail->o_free[par], ((rd.n - 2) >> 1) & 1)) break;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        if (c < nch) {
+          const float w = warp_sum8(&l[c * 8], lane);
+          if ((lane & 3) == 0) tail->lsum[par][q4][r0 + c * 8 + (lane >> 2)] = w;
+        }
+      if (key < nch * 8) tail->ref[par][r0 + key] = -tail->nref[r0 + key];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->l_full[par]));
+      rd.release(tail->sched);
+    }
+    if (!voted_out) vote(!finished);
+  } else {
+    regs_dec<kRegsOutput>();
+    // ------------------------------------------------------------ output
+    const int q4 = warp & 3, d = q4 * 32 + lane;   // d: column of the output = TMEM lane
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    SegReader rd;
+    uint32_t syncs = 0;
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail->esync));
+      return KS_PAGED_WAIT(tail->esync, syncs++ & 1);
+    };
+    while (true) {
+      const Seg* cur = rd.peek(p, tail->sched, abort);
+      if (!cur || cur->nb == 0) break;
+      const Seg& s = *cur;
+      const uint32_t par = rd.n & 1, phase = (rd.n >> 1) & 1;
+      const int rows = s.tokens * p.grp;
+      const bool cut = s.nb < s.blocks;
+      unsigned char* pc = own_piece(p, s);
+      int hh = 0;
+      float* part = reinterpret_cast<float*>(pc + kPieceStats) + d;
+      __nv_bfloat16* dst = p.out + ((long long)s.row0 * p.Hq + s.g * p.grp) * HD + d;
+      const long long next = (long long)(p.Hq - p.grp + 1) * HD;
+      if (!KS_PAGED_WAIT(tail->l_full[par], phase)) break;
+      float inv[2];                            // of rows lane and lane + 32
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = lane + 32 * h;
         const float sum = (tail->lsum[par][0][r] + tail->lsum[par][1][r]) +
                           (tail->lsum[par][2][r] + tail->lsum[par][3][r]);
-        tail->inv[r] = sum > 0.f ? 1.0f / sum : 0.f;
-        if (cut) __stcg(reinterpret_cast<float2*>(pc) + r, make_float2(tail->ref[par][r], sum));
+        inv[h] = sum > 0.f ? 1.0f / sum : 0.f;
+        if (cut && q4 == 0 && r < rows)
+          __stcg(reinterpret_cast<float2*>(pc) + r, make_float2(tail->ref[par][r], sum));
       }
-      if (!wait_pv(last_j) || !meet()) return false;
-      float* part = reinterpret_cast<float*>(pc + kPieceStats) + r0 * HD + key;
-      int hh = r0 % p.grp;
-      __nv_bfloat16* dst =
-          p.out + ((long long)(t.row0 + r0 / p.grp) * p.Hq + t.g * p.grp + hh) * HD + key;
-      const long long next = (long long)(p.Hq - p.grp + 1) * HD;
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        if (c >= nch) break;
+      if (!KS_PAGED_WAIT(tail->o_full[par], phase)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 8) {
         float o[8];
-        tmem_ld8(tmem + lanes + kO + par * 64 + r0 + c * 8, o);
+        tmem_ld8(tmem + lanes + kO + par * 64 + r0, o);
         tmem_wait_ld();
         reg_fence8(o);
-        if (key < HD)
+        const float iv = r0 < 32 ? inv[0] : inv[1];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (r0 + c * 8 + e >= rows) break;
+        for (int e = 0; e < 8; ++e) {
+          const float f = __shfl_sync(0xffffffffu, iv, (r0 + e) & 31);
+          if (r0 + e < rows && d < HD) {
             if (cut) {
-              __stcg(part + (c * 8 + e) * HD, o[e]);
+              __stcg(part + (r0 + e) * HD, o[e]);
             } else {
-              *dst = __float2bfloat16_rn(o[e] * tail->inv[r0 + c * 8 + e]);
+              *dst = __float2bfloat16_rn(o[e] * f);
               if (++hh == p.grp) {
                 hh = 0;
                 dst += next;
@@ -419,220 +598,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail->o_free[par]));
       if (cut) {
-        if (!meet_all()) return false;
-        if (warp == 4 && lane == 0) tail->last = arrive_piece(p, t);
-        if (!meet_all()) return false;
-        if (tail->last) join_pieces<HD>(p, t, warp - 4, 8, lane);
+        if (!meet()) break;
+        if (warp == 12 && lane == 0) tail->last = arrive_piece(p, s);
+        if (!meet()) break;
+        if (tail->last) join_pieces<HD>(p, s, q4, 4, lane);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tail->sched.empty[pn % kSegRing]));
-      return true;
-    };
-    while (ok) {
-      const Seg* cur = rd.peek(p, tail->sched, abort);
-      if (!cur) break;
-      ++rd.n;
-      const Seg& s = *cur;
-      const int nb = s.nb;                     // 0 at the end of the share
-      const uint32_t par = (rd.n - 1) & 1, to_o = tmem + lanes + kO + par * 64;
-      const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
-      const int r0 = G ? half * 8 : 0;         // this group's first row
-      const int nch = G ? chunks - half : half;
-      float l[CPG];
-#pragma unroll
-      for (int c = 0; c < CPG; ++c) l[c] = 0.f;
-      for (int i = 0; i == 0 || i < nb; ++i) {
-        const uint32_t b = j & 1;
-        if (nb > 0) {
-          if (!KS_PAGED_WAIT(tail->s_full[b], (j >> 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          float sc[CPG];
-#pragma unroll
-          for (int c = 0; c < NCH; ++c)
-            if (c < nch) tmem_ld8(tmem + lanes + kS + b * 128 + r0 + c * 8, &sc[c * 8]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < NCH; ++c) reg_fence8(&sc[c * 8]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[b]));   // S_{j+2} may be computed now
-          if (nch > 0) {
-            const int kb = s.key_block(i);
-            if (s.masked(p, kb)) {
-              // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
-              // on, and while the key is in its window up to row (k - p_first + window) grp
-              const int k = kb * kBlock + key;
-              const long long d = (long long)k - s.p_first;
-              const int from = (int)(d < 0 ? 0 : d > 128 ? 128 : d) * p.grp;
-              int to = 1 << 20;
-              if (p.window > 0 && k >= p.sinks) {
-                const long long e = d + p.window;
-                to = (int)(e < 0 ? 0 : e > 128 ? 128 : e) * p.grp;
-              }
-#pragma unroll
-              for (int c = 0; c < CPG; ++c)
-                if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;
-            }
-            if (i == 0) {
-              // a piece's first references: the largest score of four of its keys will do, since
-              // a row's P and sums may grow to 2^kStale times the reference's before it moves
-              if (lane == 0) {
-#pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                  if (c < nch)
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4)
-                      *reinterpret_cast<float4*>(&tail->wmax[q4][r0 + c * 8 + e]) = make_float4(
-                          sc[c * 8 + e], sc[c * 8 + e + 1], sc[c * 8 + e + 2], sc[c * 8 + e + 3]);
-              }
-              if (!meet()) {
-                ok = false;
-                break;
-              }
-              if (key < nch * 8) {
-                const int r = r0 + key;
-                const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
-                                             fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
-                tail->nref[r] = -fmaxf(mx, kNoRef);
-              }
-              if (!meet()) {
-                ok = false;
-                break;
-              }
-            }
-            // has a score outgrown its row's reference?
-            bool any = false;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-              if (c < nch) {
-                const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-                const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
-                const float* x = &sc[c * 8];
-                const float m0 =
-                    fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
-                const float m1 =
-                    fmax3(fmaf(x[3], sl2, n0.w), fmaf(x[4], sl2, n1.x), fmaf(x[5], sl2, n1.y));
-                any |= fmax3(m0, m1, fmaxf(fmaf(x[6], sl2, n1.z), fmaf(x[7], sl2, n1.w))) > kStale;
-              }
-            any = __any_sync(0xffffffffu, any);
-            const int votes = vote(any && lane == 0);
-            if (votes >= 32) {
-              ok = false;
-              break;
-            }
-            const bool grow = votes > 0;
-            if (grow) {
-              // maxima over the keys, and the rows' new references
-#pragma unroll
-              for (int c0 = 0; c0 < CPG; c0 += 32) {
-                float m = 0.f;
-#pragma unroll
-                for (int c = c0; c < c0 + 32 && c < CPG; ++c)
-                  if (c < nch * 8) {
-                    const float w = warp_max(sc[c]);
-                    if (lane == c - c0) m = w;
-                  }
-                if (c0 + lane < nch * 8) tail->wmax[q4][r0 + c0 + lane] = m;
-              }
-              if (!meet()) {
-                ok = false;
-                break;
-              }
-              if (key < nch * 8) {
-                const int r = r0 + key;
-                const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
-                                             fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
-                const float old = -tail->nref[r];
-                const bool up = mx - old > kStale;
-                tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
-                tail->nref[r] = up ? -mx : -old;
-              }
-              if (!meet()) {
-                ok = false;
-                break;
-              }
-              if (i > 0) {
-                // sums and O hold the blocks before relative to the old references
-                if (!wait_pv(j - 1)) {
-                  ok = false;
-                  break;
-                }
-#pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                  if (c < nch) {
-                    float v[8];
-                    const uint32_t to = to_o + r0 + c * 8;
-                    tmem_ld8(to, v);
-                    tmem_wait_ld();
-                    reg_fence8(v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                      const float a = tail->alpha[r0 + c * 8 + e];
-                      v[e] *= a;
-                      l[c * 8 + e] *= a;
-                    }
-                    tmem_st8(to, v);
-                  }
-                tmem_wait_st();
-              }
-            }
-            // the P buffer was last read by PV_{j-2}
-            if (j >= 2 && !wait_pv(j - 2)) {
-              ok = false;
-              break;
-            }
-            unsigned char* pt = smem + off_p + b * p_tile + p_key + r0 * 128;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-              if (c < nch) {
-                const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-                const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
-                const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float w = ex2(fmaf(sc[c * 8 + e], sl2, n[e]));
-                  l[c * 8 + e] += w;
-                  *reinterpret_cast<__nv_bfloat16*>(pt + (c * 8 + e) * 128 + ((p_chunk ^ e) << 4)) =
-                      __float2bfloat16_rn(w);
-                }
-              }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          } else if (j >= 2 && !wait_pv(j - 2)) {   // keep in step
-            ok = false;
-            break;
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&tail->p_full[b]));
-          ++j;
-        }
-        if (pending && !(ok = finish())) break;
-      }
-      if (!ok) break;
-      if (nb == 0) {
-        finished = true;
-        break;
-      }
-      // the piece's sums and references, for finish()
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-        if (c < nch) {
-          const float w = warp_sum8(&l[c * 8], lane);
-          if ((lane & 3) == 0) tail->lsum[par][q4][r0 + c * 8 + (lane >> 2)] = w;
-        }
-      if (key < nch * 8) tail->ref[par][r0 + key] = -tail->nref[r0 + key];
-      pending = true;
-      last_j = j - 1;
+      rd.release(tail->sched);
     }
-    if (!voted_out) vote(!finished);
   }
 
   tc_fence_before();
@@ -649,6 +627,13 @@ ks_status launch(Params p, const CUtensorMap& tq, const CUtensorMap& tk, const C
   static std::atomic<unsigned long long> attr{0};
   auto k = paged_decode_kernel<HD, CPG>;
   KS_TRY(once_per_device(attr, [&]() -> ks_status {
+    // the setmaxnreg split assumes exactly kRegs registers a thread at launch
+    cudaFuncAttributes fa;
+    KS_CUDA_TRY(cudaFuncGetAttributes(&fa, k));
+    if (fa.numRegs != kRegs)
+      return fail(KS_ERR_INTERNAL, "paged attention: kernel built with " + std::to_string(fa.numRegs) +
+                                       " registers a thread, the register split needs " +
+                                       std::to_string(kRegs));
     KS_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
     return KS_OK;
   }));

@@ -27,8 +27,7 @@ using namespace sm100;
 constexpr int kBlock = 128;                  // keys per block
 constexpr int kMaxCtas = 148;                // one CTA per SM of a B200
 constexpr int kTileRows = 128;               // query rows of a tile, at most
-constexpr int kThreads = 384;                // both kernels: 12 warps
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 16;
 constexpr float kNoRef = -1e30f;             // reference of a row that has seen no key
 
 // Workspace: one arrival counter per CTA (of the unit whose first piece it
@@ -45,7 +44,8 @@ struct Params {
   unsigned char* ws;
   int32_t* status;
   int B, n_tokens, max_new, max_blocks, cap;   // cap = max_blocks * page_size positions a row
-  int Hq, Hkv, grp, page_size, n_pages, n_slots, box;   // box: keys per TMA box
+  int Hq, Hkv, grp, page_size, n_pages, n_slots;
+  int box, log2_boxes;                         // keys of a TMA box, boxes of a block
   int window, sinks;
   int tile_tokens;                             // tokens per query tile
   int q_rows;                                  // decode kernel: rows of a Q / P tile (N)
@@ -100,7 +100,7 @@ __device__ __forceinline__ Tile make_tile(const Params& p, const Req& r, int til
 }
 
 __device__ __forceinline__ int n_tiles(const Params& p, const Req& r) {
-  return (r.n + p.tile_tokens - 1) / p.tile_tokens;
+  return r.n <= p.tile_tokens ? (r.n > 0) : (r.n + p.tile_tokens - 1) / p.tile_tokens;
 }
 
 // One piece of a unit, as the roles of a CTA read it from the ring.
@@ -109,7 +109,8 @@ struct alignas(16) Seg {
   int p_first, p_last, lo, sinks;
   int sink_blocks, k0, nb, blocks;             // blocks k0 .. k0+nb-1 of the unit's `blocks`; nb = 0 ends
   int first_cta, pieces;                       // of a cut unit (pieces = 1 otherwise)
-  int pad0, pad1;
+  int lead, trail;                             // unit blocks k with some key hidden from some token:
+                                               // k < lead or k >= trail
   __device__ __forceinline__ int key_block(int i) const {   // i counts from k0
     const int k = k0 + i;
     return k < sink_blocks ? k : lo / kBlock + (k - sink_blocks);
@@ -118,12 +119,7 @@ struct alignas(16) Seg {
   __device__ __forceinline__ bool unseen(int j0, int j1) const {
     return j0 > p_last || (j1 < lo && j0 >= sinks);
   }
-  // Some key of this block is hidden from some token.
-  __device__ __forceinline__ bool masked(const Params& p, int kb) const {
-    const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
-    return j1 > p_first ||
-           (p.window > 0 && p_last >= p.window && j0 <= p_last - p.window && j1 >= p.sinks);
-  }
+  __device__ __forceinline__ bool masked(int i) const { return k0 + i < lead || k0 + i >= trail; }
   // Some key of this block is hidden from every token.
   __device__ __forceinline__ bool ragged(int kb) const {
     const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
@@ -132,7 +128,7 @@ struct alignas(16) Seg {
 };
 static_assert(sizeof(Seg) == 64, "segments are copied as four uint4");
 
-constexpr int kSegRing = 4;
+constexpr int kSegRing = 8;
 
 struct Start {                                 // where a CTA's share begins
   long long first, end, total;                 // block numbers; total = all blocks
@@ -143,8 +139,10 @@ struct Start {                                 // where a CTA's share begins
 struct SchedSmem {
   Seg seg[kSegRing];
   uint64_t full[kSegRing], empty[kSegRing];
-  Start start;
-  long long warp_sum[kWarps];
+  Start start;                                 // later: where the walk stands
+  Req held[32];                                // requests base .. base + 31
+  int base, published;
+  long long warp_sum[kMaxWarps];
 };
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
@@ -189,11 +187,12 @@ __device__ __forceinline__ long long head_blocks(const Params& p, const Req& r, 
   return w;
 }
 
-// Finds the CTA's share (all threads; sm.start is valid after the caller's next
+// Finds the CTA's share (all W warps; sm.start is valid after the caller's next
 // __syncthreads).
+template <int W>
 __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (p.B + kWarps - 1) / kWarps;
+  const int per = (p.B + W - 1) / W;
   const int r0 = min(warp * per, p.B), r1 = min(r0 + per, p.B);
   long long mine = 0, w_first = 0;
   Req r_first{0, 0, 0};
@@ -214,7 +213,7 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
   __syncthreads();
   long long total = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w == warp) before = total;
     total += sm.warp_sum[w];
   }
@@ -264,50 +263,41 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
 // Warp-uniform wait that also reports a lane's timeout to the others.
 #define KS_PAGED_WAIT(bar, parity) warp_wait(smem_u32(&(bar)), (uint32_t)(parity), abort, p.status)
 
-// Walks a CTA's share and publishes its pieces, then an end mark (one warp, which
-// also loads the keys: a piece is published when its first key block is next).
-struct Walker {
-  long long at;
-  int b, g, tile, k, base;
-  Req held;                                    // lane l holds request base + l
-  uint32_t n;
-  __device__ __forceinline__ void hold(const Params& p) {
-    const int r = base + (threadIdx.x & 31);
-    bool bad;
-    held = Req{0, 0, 0};
-    if (r < p.B) held = load_req(p, r, &bad);
-  }
-  __device__ __forceinline__ void start(const Params& p, const SchedSmem& sm) {
-    at = sm.start.first;
-    b = base = sm.start.b;
-    g = sm.start.g;
-    tile = sm.start.tile;
-    k = sm.start.k;
-    n = 0;
-    if (at < sm.start.end) hold(p);
-  }
-  // The next piece in the ring (nb = 0: the end), or NULL to give up.
-  __device__ __forceinline__ const Seg* next(const Params& p, SchedSmem& sm, volatile int* abort) {
-    const int lane = threadIdx.x & 31, slot = n % kSegRing;
-    if (!KS_PAGED_WAIT(sm.empty[slot], ((n / kSegRing) & 1) ^ 1)) return nullptr;
-    ++n;
-    Seg* seg = &sm.seg[slot];
-    const long long end = sm.start.end;
-    if (at >= end || b >= p.B) {
-      if (lane == 0) {
-        seg->nb = 0;
-        mbar_arrive(smem_u32(&sm.full[slot]));
-      }
-      __syncwarp();
-      return seg;
-    }
-    const Req r = shfl_req(held, b - base);
-    const Tile t = make_tile(p, r, tile);
-    const int nb = (int)(end - at < t.blocks - k ? end - at : t.blocks - k);
-    if (lane == 0) {
+// The walk over a CTA's share, by the warp that loads its keys.  Its state lies in
+// shared memory: the loading loop has few registers.
+__device__ __forceinline__ void hold_requests(const Params& p, SchedSmem& sm, int base, int lane) {
+  bool bad;
+  Req r{0, 0, 0};
+  if (base + lane < p.B) r = load_req(p, base + lane, &bad);
+  sm.held[lane] = r;
+  if (lane == 0) sm.base = base;
+  __syncwarp();
+}
+__device__ __forceinline__ void start_walk(const Params& p, SchedSmem& sm, int lane) {
+  if (sm.start.first < sm.start.end) hold_requests(p, sm, sm.start.b, lane);
+  if (lane == 0) sm.published = 0;
+  __syncwarp();
+}
+// Publishes the next piece (nb = 0: the end) and returns it, or NULL to give up.
+__device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volatile int* abort) {
+  const int lane = threadIdx.x & 31, n = sm.published, slot = n % kSegRing;
+  if (!KS_PAGED_WAIT(sm.empty[slot], ((n / kSegRing) & 1) ^ 1)) return nullptr;
+  Seg* seg = &sm.seg[slot];
+  Start& st = sm.start;
+  const bool over = st.first >= st.end || st.b >= p.B;
+  bool next_request = false;
+  if (lane == 0) {
+    sm.published = n + 1;
+    if (over) {
+      seg->nb = 0;
+    } else {
+      const Req r = sm.held[st.b - sm.base];
+      const Tile t = make_tile(p, r, st.tile);
+      const long long at = st.first;
+      const int k = st.k, nb = (int)(st.end - at < t.blocks - k ? st.end - at : t.blocks - k);
       Seg s;
-      s.b = b;
-      s.g = g;
+      s.b = st.b;
+      s.g = st.g;
       s.row0 = t.row0;
       s.tokens = t.tokens;
       s.p_first = t.p_first;
@@ -320,36 +310,49 @@ struct Walker {
       s.blocks = t.blocks;
       s.first_cta = blockIdx.x;
       s.pieces = 1;
-      s.pad0 = s.pad1 = 0;
+      // keys up to p_first are below the causal edge of every token; the window's lower edge
+      // crosses the blocks from lo's to the one of the last token's first key
+      const int b0 = t.lo / kBlock;
+      s.trail = t.p_first < 0 ? 0 : t.sink_blocks + max(0, (t.p_first + 1) / kBlock - b0);
+      s.lead = p.window > 0 && t.p_last >= p.window
+                   ? t.sink_blocks + (t.p_last - p.window) / kBlock + 1 - b0
+                   : 0;
       if (nb < t.blocks) {
         // block x belongs to CTA ((x + 1) ctas - 1) / total
-        const long long u0 = at - k, u1 = u0 + t.blocks, total = sm.start.total;
-        const int ctas = sm.start.ctas;
-        s.first_cta = (int)(((u0 + 1) * ctas - 1) / total);
-        s.pieces = (int)((u1 * ctas - 1) / total) - s.first_cta + 1;
+        const long long u0 = at - k, u1 = u0 + t.blocks;
+        s.first_cta = (int)(((u0 + 1) * st.ctas - 1) / st.total);
+        s.pieces = (int)((u1 * st.ctas - 1) / st.total) - s.first_cta + 1;
       }
       *seg = s;
-      mbar_arrive(smem_u32(&sm.full[slot]));
-    }
-    __syncwarp();
-    at += nb;
-    k = 0;
-    if (++tile == n_tiles(p, r)) {
-      tile = 0;
-      if (++g == p.Hkv) {
-        g = 0;
-        for (++b; b < p.B; ++b) {              // the next request with a token
-          if (b - base == 32) {
-            base = b;
-            hold(p);
-          }
-          if (__shfl_sync(0xffffffffu, held.n, b - base) > 0) break;
+      st.first = at + nb;
+      st.k = 0;
+      if (++st.tile == n_tiles(p, r)) {
+        st.tile = 0;
+        if (++st.g == p.Hkv) {
+          st.g = 0;
+          next_request = true;
         }
       }
     }
-    return seg;
+    mbar_arrive(smem_u32(&sm.full[slot]));
   }
-};
+  __syncwarp();
+  if (__shfl_sync(0xffffffffu, (int)next_request, 0)) {   // the next request with a token
+    int b = st.b + 1, base = sm.base;
+    for (; b < p.B; ++b) {
+      if (b - base == 32) {
+        __syncwarp();
+        base = b;
+        hold_requests(p, sm, base, lane);
+      }
+      if (sm.held[b - base].n > 0) break;
+    }
+    __syncwarp();
+    if (lane == 0) st.b = b;
+    __syncwarp();
+  }
+  return seg;
+}
 
 // A role's reader of the ring: take() copies the next piece (false: give up);
 // one lane of each role must be counted in the ring's `empty` barriers.
@@ -379,27 +382,93 @@ struct SegReader {
   }
 };
 
-// The pool row (slot) of the first key of this lane's TMA box: lane l loads box
-// l % 16 of panel l / 16.  A box that no token of the tile sees and a page that
-// is none read past the pool, where the tensor map gives zeros without touching
-// memory.  fetch() only loads the table entry, so that it can run a block ahead.
-struct BoxRow {
-  int page, row;                               // row inside the page; -1: unseen
-  __device__ __forceinline__ void fetch(const Params& p, const Seg& s, int kb, int lane) {
-    const int off = (lane & 15) * p.box, j0 = kb * kBlock + off;
-    row = -1;
-    if (off >= kBlock || s.unseen(j0, j0 + p.box - 1)) return;
+// Where the boxes of a piece's key blocks lie in the pool.  A block has n boxes
+// (each inside one page); lane l looks up box l % n of block i + l / n, so one fetch
+// serves 32 / n blocks, and it is asked for that long before its use: under load a
+// table entry takes microseconds to come.  A box that no token of the tile sees and
+// a page that is none give a row past the pool, where the tensor map reads zeros
+// without touching memory.
+struct BoxRows {
+  int page, in_page;                           // of the fetch under way; in_page < 0: unseen
+  int rows;                                    // first pool row of the lane's box, after use()
+  __device__ __forceinline__ void fetch(const Params& p, const Seg& s, int i, int lane) {
+    i += lane >> p.log2_boxes;
+    in_page = -1;
+    if (i >= s.nb) return;
+    const int j0 = s.key_block(i) * kBlock + (lane & ((1 << p.log2_boxes) - 1)) * p.box;
+    if (s.unseen(j0, j0 + p.box - 1)) return;
     const int blk = j0 / p.page_size;          // a key that is seen lies inside the table's row
-    row = j0 - blk * p.page_size;
+    in_page = j0 - blk * p.page_size;
     page = p.table[(long long)s.b * p.max_blocks + blk];
   }
-  __device__ __forceinline__ int slot(const Params& p) const {
-    if (row < 0) return p.n_slots;
-    if ((unsigned)page < (unsigned)p.n_pages) return page * p.page_size + row;
-    raise_status(p.status, KS_ERR_INVALID_ARG);
-    return p.n_slots;
+  __device__ __forceinline__ void use(const Params& p) {
+    rows = p.n_slots;
+    if (in_page < 0) return;
+    if ((unsigned)page < (unsigned)p.n_pages) rows = page * p.page_size + in_page;
+    else raise_status(p.status, KS_ERR_INVALID_ARG);
   }
 };
+
+// One warp that loads the share's K blocks (and walks it) or its V blocks into a
+// ring; lane l loads the box l % 16 of panel l / 16.  on_piece(s), K only: before a
+// piece's first block; false gives up.
+struct Ring {
+  const CUtensorMap* tm;
+  uint64_t *full, *empty;
+  uint32_t base;                               // shared address of slot 0
+  int slots, stride;
+};
+template <int HD, typename F>
+__device__ __forceinline__ void load_share(const Params& p, SchedSmem& sm, const Ring& r, bool is_k,
+                                           volatile int* abort, F&& on_piece) {
+  constexpr int PANELS = HD / 64;
+  const int lane = threadIdx.x & 31, lb = p.log2_boxes, per = 32 >> lb;
+  const bool mine = (lane & 15) >> lb == 0 && (lane >> 4) < PANELS;
+  const uint32_t box_off = r.base + (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
+  if (is_k) start_walk(p, sm, lane);
+  SegReader rd;
+  int slot = 0, n_loads = 0;
+  uint32_t phase = 1;
+  BoxRows at;
+  const Seg* s = is_k ? walk(p, sm, abort) : rd.peek(p, sm, abort);
+  if (s && s->nb > 0) at.fetch(p, *s, 0, lane);
+  while (s && s->nb > 0) {
+    if (is_k && !on_piece(*s)) break;
+    const Seg* following = nullptr;
+    const int nb = s->nb, x = s->g * HD + (lane >> 4) * 64;
+    int i = 0;
+    do {
+      at.use(p);
+      const int m = min(per, nb - i);
+      if (i + m < nb) at.fetch(p, *s, i + m, lane);
+      int e = 0;
+      for (; e < m; ++e) {
+        if (!KS_PAGED_WAIT(r.empty[slot], phase)) break;
+        const uint32_t fb = smem_u32(&r.full[slot]);
+        const int row = __shfl_sync(0xffffffffu, at.rows, (e << lb) + (lane & ((1 << lb) - 1)));
+        if (lane == 0) mbar_arrive_expect_tx(fb, PANELS * kBlock * 128);
+        __syncwarp();
+        if (mine) tma_load_2d(box_off + slot * r.stride, r.tm, x, row, fb);
+        ++n_loads;
+        if (++slot == r.slots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (e < m) break;
+      i += m;
+    } while (i < nb);
+    if (i < nb) break;
+    if (!is_k) rd.release(sm);
+    following = is_k ? walk(p, sm, abort) : rd.peek(p, sm, abort);
+    if (following && following->nb > 0) at.fetch(p, *following, 0, lane);
+    s = following;
+  }
+  // wait for the copies still in flight before leaving
+  if (lane == 0)
+    for (int n = n_loads > r.slots ? n_loads - r.slots : 0; n < n_loads; ++n)
+      mbar_wait_drain(smem_u32(&r.full[n % r.slots]), (uint32_t)(n / r.slots) & 1, p.status);
+}
 
 // Zeroes the rows of a V block that no token of the tile sees (their weights are
 // zero, but zero times what the page holds there need not be); one warp.  Boxes of
