@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &tail->abort;
   const uint32_t sbase = smem_u32(smem);
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kThreads - 32) {          // the first warps have requests to read
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);

@@ -145,6 +145,12 @@ struct SchedSmem {
   long long warp_sum[kMaxWarps];
 };
 
+// Quotient of non-negative numbers.  Block numbers almost always fit 32 bits, and a
+// 64-bit division costs hundreds of cycles of a kernel that may take ten thousand.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -199,9 +205,10 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
   for (int base = r0; base < r1; base += 32) {
     Req r{0, 0, 0};
     bool bad = false;
-    if (base + lane < r1) r = load_req(p, base + lane, &bad);
+    if (base + lane < p.B) r = load_req(p, base + lane, &bad);
     if (bad) raise_status(p.status, KS_ERR_INVALID_ARG);
-    const long long w = head_blocks(p, r, lane) * p.Hkv;
+    // lanes past r1 hold another warp's requests, which the walk may come to
+    const long long w = head_blocks(p, base + lane < r1 ? r : Req{0, 0, 0}, lane) * p.Hkv;
     if (base == r0) {
       r_first = r;
       w_first = w;
@@ -209,7 +216,10 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
     mine += warp_sum_ll(w);
   }
   if (lane == 0) sm.warp_sum[warp] = mine;
-  if (threadIdx.x == 0) sm.start.first = sm.start.end = 0;
+  if (threadIdx.x == 0) {
+    sm.start.first = sm.start.end = 0;
+    sm.published = 0;
+  }
   __syncthreads();
   long long total = 0, before = 0;
 #pragma unroll
@@ -220,7 +230,7 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
   const int ctas = (int)(total < gridDim.x ? total : gridDim.x);
   const int c = blockIdx.x;
   if (c >= ctas) return;                       // no share (or no work at all)
-  const long long first = total * c / ctas, end = total * (c + 1) / ctas;
+  const long long first = quotient(total * c, ctas), end = quotient(total * (c + 1), ctas);
   if (first < before || first >= before + mine) return;
   long long at = before;
   for (int base = r0; base < r1; base += 32) {
@@ -229,8 +239,8 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
     if (base != r0) {
       bool bad;
       r = Req{0, 0, 0};
-      if (base + lane < r1) r = load_req(p, base + lane, &bad);
-      w = head_blocks(p, r, lane) * p.Hkv;
+      if (base + lane < p.B) r = load_req(p, base + lane, &bad);
+      w = head_blocks(p, base + lane < r1 ? r : Req{0, 0, 0}, lane) * p.Hkv;
     }
     const long long upto = at + warp_scan_ll(w, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, first < upto);
@@ -240,9 +250,9 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
     }
     const int src = __ffs(hit) - 1;
     const Req q = shfl_req(r, src);
-    const long long head = __shfl_sync(0xffffffffu, w, src) / p.Hkv;
+    const long long head = quotient(__shfl_sync(0xffffffffu, w, src), p.Hkv);
     const long long off = first - __shfl_sync(0xffffffffu, upto - w, src);
-    const int g = (int)(off / head), T = n_tiles(p, q);
+    const int g = (int)quotient(off, head), T = n_tiles(p, q);
     long long rest = off - g * head;
     for (int t0 = 0; t0 < T; t0 += 32) {
       const long long nb = t0 + lane < T ? make_tile(p, q, t0 + lane).blocks : 0;
@@ -251,7 +261,11 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
       if (in) {
         const int l = __ffs(in) - 1;
         const int k = (int)(rest - __shfl_sync(0xffffffffu, s - nb, l));
-        if (lane == 0) sm.start = Start{first, end, total, ctas, base + src, g, t0 + l, k};
+        sm.held[lane] = r;                     // the walk begins with these requests
+        if (lane == 0) {
+          sm.start = Start{first, end, total, ctas, base + src, g, t0 + l, k};
+          sm.base = base;
+        }
         return;
       }
       rest -= __shfl_sync(0xffffffffu, s, 31);
@@ -271,11 +285,6 @@ __device__ __forceinline__ void hold_requests(const Params& p, SchedSmem& sm, in
   if (base + lane < p.B) r = load_req(p, base + lane, &bad);
   sm.held[lane] = r;
   if (lane == 0) sm.base = base;
-  __syncwarp();
-}
-__device__ __forceinline__ void start_walk(const Params& p, SchedSmem& sm, int lane) {
-  if (sm.start.first < sm.start.end) hold_requests(p, sm, sm.start.b, lane);
-  if (lane == 0) sm.published = 0;
   __syncwarp();
 }
 // Publishes the next piece (nb = 0: the end) and returns it, or NULL to give up.
@@ -320,8 +329,8 @@ __device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volat
       if (nb < t.blocks) {
         // block x belongs to CTA ((x + 1) ctas - 1) / total
         const long long u0 = at - k, u1 = u0 + t.blocks;
-        s.first_cta = (int)(((u0 + 1) * st.ctas - 1) / st.total);
-        s.pieces = (int)((u1 * st.ctas - 1) / st.total) - s.first_cta + 1;
+        s.first_cta = (int)quotient((u0 + 1) * st.ctas - 1, st.total);
+        s.pieces = (int)quotient(u1 * st.ctas - 1, st.total) - s.first_cta + 1;
       }
       *seg = s;
       st.first = at + nb;
@@ -425,7 +434,6 @@ __device__ __forceinline__ void load_share(const Params& p, SchedSmem& sm, const
   const int lane = threadIdx.x & 31, lb = p.log2_boxes, per = 32 >> lb;
   const bool mine = (lane & 15) >> lb == 0 && (lane >> 4) < PANELS;
   const uint32_t box_off = r.base + (lane >> 4) * (kBlock * 128) + (lane & 15) * p.box * 128;
-  if (is_k) start_walk(p, sm, lane);
   SegReader rd;
   int slot = 0, n_loads = 0;
   uint32_t phase = 1;
