@@ -88,6 +88,65 @@ def test_causal_attention_over_pages(i, ws):
     assert torch.equal(_attend(L, q, kp, vp, ws)[0], out)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("heads,new", [((8, 2), n) for n in (2, 4, 5, 8, 9, 12, 16, 17, 32, 33)]
+                         + [((10, 2), 13), ((10, 2), 26), ((7, 1), 10), ((6, 2), 43), ((31, 1), 2),
+                            ((33, 1), 2), ((100, 1), 1), ((65, 1), 1)])
+def test_row_counts_around_the_tile_sizes(heads, new, hd, ws):
+    """Query rows per kv head on both sides of 16, 32, 64 and 128, of full and of
+    short chunks in one step; the pages divide neither a block nor each other."""
+    Hq, Hkv = heads
+    L = P.Layout([(333, new), (0, max(1, new - 1)), (1500, 1), (127, new), (640, 0), (129, 1)], 40,
+                 seed=new)
+    kp, vp = L.pool(Hkv, hd), L.pool(Hkv, hd, seed=2)
+    q = _queries(L, Hq, hd)
+    for window, sinks in ((0, 0), (150, 3)):
+        out, st = _attend(L, q, kp, vp, ws, window, sinks)
+        _within(out, *P.attention_reference(L, q, kp, vp, window, sinks))
+        assert st.item() == 0
+
+
+@pytest.mark.parametrize("page", [8, 40, 56, 96, 128, 384, 1024])
+@pytest.mark.parametrize("new", [3, 70])
+def test_page_sizes(page, new, ws):
+    L = P.Layout([(1000, new), (page, 1), (page - 1, 2), (3 * page + 5, new)], page, seed=page)
+    kp, vp = L.pool(2, 128), L.pool(2, 128, seed=2)
+    q = _queries(L, 8, 128)
+    out, st = _attend(L, q, kp, vp, ws)
+    _within(out, *P.attention_reference(L, q, kp, vp))
+    assert st.item() == 0
+
+
+def test_many_requests_mostly_idle(ws):
+    g = torch.Generator().manual_seed(7)
+    n = (torch.rand(5000, generator=g) < 0.1).long().tolist()
+    c = torch.randint(0, 300, (5000,), generator=g).tolist()
+    lens = [(ci if ni else 0, ni) for ci, ni in zip(c, n)]
+    lens[-1] = (4000, 1)
+    L = P.Layout(lens, 16)
+    kp, vp = L.pool(1, 64), L.pool(1, 64, seed=2)
+    q = _queries(L, 2, 64)
+    out, st = _attend(L, q, kp, vp, ws)
+    _within(out, *P.attention_reference(L, q, kp, vp))
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_pool_past_32_bit_offsets(new, ws):
+    """Pages behind the 2^31st element of a pool (4.3 GB each of K and V)."""
+    Hkv, hd, page = 8, 128, 64
+    L = P.Layout([(700, new), (130, 1)], page)
+    n_pages = (1 << 31) // (page * Hkv * hd) + L.n_pages
+    kp, vp = (torch.empty(n_pages, page, Hkv, hd, dtype=P.BF16, device="cuda") for _ in range(2))
+    first = n_pages - L.n_pages
+    kp[first:], vp[first:] = L.pool(Hkv, hd), L.pool(Hkv, hd, seed=2)
+    q = _queries(L, 32, hd)
+    table = torch.where(L.table >= 0, L.table + first, L.table)
+    out, st = _attend(L, q, kp, vp, ws, table=table)
+    _within(out, *P.attention_reference(L, q, kp[first:], vp[first:]))
+    assert st.item() == 0
+
+
 # (lens, heads, page, window, sinks)
 WINDOWED = [
     ([(0, 1), (5, 1), (400, 1)], (4, 4, 64), 16, 1, 0),
@@ -218,6 +277,45 @@ def test_bad_pages_and_lengths_are_reported(ws):
     # and the next call is a good one again
     out, st = _attend(L, q, kp, vp, ws)
     assert st.item() == 0 and torch.equal(out, good)
+
+
+@pytest.mark.parametrize("new,fill", [(1, 0x7F), (1, 0xFF), (60, 0x7F)])
+def test_a_workspace_that_does_not_start_out_zero_is_reported(new, fill):
+    L = P.Layout([(9000, new)], 64)            # long enough to be cut into pieces
+    kp, vp = L.pool(2, 128), L.pool(2, 128, seed=2)
+    q = _queries(L, 8, 128)
+    w = B.paged_attention_workspace().fill_(fill)
+    assert _attend(L, q, kp, vp, w)[1].item() == 3
+    w.zero_()
+    out, st = _attend(L, q, kp, vp, w)
+    _within(out, *P.attention_reference(L, q, kp, vp))
+    assert st.item() == 0
+
+
+def test_one_workspace_serves_calls_of_every_shape(ws):
+    """Large, small, cut and uncut steps one after the other, without clearing."""
+    for i in (9, 0, 11, 14, 6, 12, 10):
+        lens, (Hq, Hkv, hd), page = PLAIN[i]
+        L = P.Layout(lens, page, seed=i)
+        kp, vp = L.pool(Hkv, hd, seed=10 + i), L.pool(Hkv, hd, seed=20 + i)
+        q = _queries(L, Hq, hd)
+        fresh = _attend(L, q, kp, vp, B.paged_attention_workspace())[0]
+        assert torch.equal(_attend(L, q, kp, vp, ws)[0], fresh)
+
+
+def test_scores_that_jump_past_every_reference(ws):
+    """A key whose score exceeds all before it by hundreds takes the whole row, at
+    the piece's start, in its middle and at its end; before it the row is even."""
+    for new, Hq in ((1, 4), (5, 8), (40, 8)):
+        for at in (3, 130, 1000, 1999):
+            L = P.Layout([(2000, new)], 32)
+            kp, vp = L.pool(2, 128, fill=0.0), L.pool(2, 128, seed=2)
+            q = _queries(L, Hq, 128).abs()
+            row = L.rows[0][at // 32]
+            kp[row, at % 32] = 60.0
+            out, st = _attend(L, q, kp, vp, ws)
+            v = vp[row, at % 32].repeat_interleave(Hq // 2, 0)
+            assert st.item() == 0 and torch.equal(out, v.expand_as(out))
 
 
 @pytest.mark.parametrize("cu", [[0, -4, 3, 6], [0, 5, 2, 6], [0, 2, 3, 900], [-3, 2, 3, 6],
