@@ -70,7 +70,7 @@ struct Cfg {
   static constexpr int OFF_TAIL = OFF_V + VST * V_SLOT;
   static constexpr int USED = OFF_TAIL + (int)((sizeof(Tail) + 255) / 256 * 256);
   static constexpr int SMEM = USED > 118784 ? USED : 118784;   // one CTA holds an SM's TMEM
-  static constexpr int REGS = 168, REGS_LOW = 56, REGS_HIGH = 224;
+  static constexpr int REGS = 168, REGS_LOW = 72, REGS_HIGH = 216;
   static_assert(128 * REGS_LOW + 256 * REGS_HIGH == kThreads * REGS, "register split");
   static constexpr int TMEM_S = 0, TMEM_P = 2 * BN, TMEM_O = 2 * BN + BN / 2;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!sp || sp->nb == 0) break;
       const Seg& s = *sp;
       const bool idle = q4 * 32 >= s.tokens * p.grp;   // no row of this warp is in the tile
+      const int lead = i0 + s.lead - s.k0, trail = i0 + s.trail - s.k0;   // blocks to mask: outside
       float m_new = kNoRef;
       for (int i = i0 + ((i0 ^ G) & 1); i < i0 + s.nb; i += 2) {
         if (!KS_PAGED_WAIT(tail->s_full[G], (i >> 1) & 1)) {
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[G]));   // S_{i+2} may be computed now
-        if (s.masked(i - i0)) {
+        if (i < lead || i >= trail) {
           const int kb = s.key_block(i - i0);
           // a row sees keys up to its position that are in its window or among the first;
           // as ranges of this block: e <= last, and e >= wlo or e < sinks

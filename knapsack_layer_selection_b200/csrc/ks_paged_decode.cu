@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = s.tokens * p.grp, chunks = (rows + 7) >> 3, half = (chunks + 1) >> 1;
       const int r0 = G ? half * 8 : 0;         // this group's first row
       const int nch = G ? chunks - half : half;
+      const int lead = s.lead - s.k0, trail = s.trail - s.k0;   // blocks to mask: outside
       float l[CPG];
 #pragma unroll
       for (int c = 0; c < CPG; ++c) l[c] = 0.f;
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[b]));   // S_{j+2} may be computed now
         if (nch > 0) {
-          if (s.masked(i)) {
+          if (i < lead || i >= trail) {
             // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
             // on, and while the key is in its window up to row (k - p_first + window) grp
             const int k = s.key_block(i) * kBlock + key;

@@ -119,7 +119,6 @@ struct alignas(16) Seg {
   __device__ __forceinline__ bool unseen(int j0, int j1) const {
     return j0 > p_last || (j1 < lo && j0 >= sinks);
   }
-  __device__ __forceinline__ bool masked(int i) const { return k0 + i < lead || k0 + i >= trail; }
   // Some key of this block is hidden from every token.
   __device__ __forceinline__ bool ragged(int kb) const {
     const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
