@@ -356,8 +356,8 @@ KS_API ks_status ks_rope_append_bf16(const void* q, int64_t q_stride, const void
  * behind cu_new[B] are left as they are.  Pages without a visible key are not
  * read (their entries may hold anything), nor does what a page holds at
  * positions that no token of the request sees, NaN included, reach a result.
- * Between tokens of one chunk the values must be finite: a key that a later
- * token sees enters an earlier one's sum with weight zero.
+ * Between tokens of one request the values must be finite: a key that one token
+ * sees enters the other tokens' sums with weight zero.
  * A page id outside the pool counts as a page of zeros and, like a request
  * whose lengths break max_new, n_tokens or max_blocks (its excess is dropped),
  * puts KS_ERR_INVALID_ARG in status.

@@ -3,10 +3,10 @@
 //
 // Work is counted in key blocks (128 positions).  A unit is one tile of query
 // rows (whole tokens x the query heads of one kv head) with the key blocks that
-// its tokens see; units are ordered by request, kv head, tile, and their blocks
-// concatenated.  CTA c takes the c-th of G equal shares of that sequence, so
-// every SM gets the same number of blocks whatever the lengths; a unit that
-// crosses a border is cut into pieces there, at most two per CTA.  The lengths
+// its tokens see, after kUnitCost blocks' worth of its own cost; units are ordered
+// by request, kv head, tile, and concatenated.  CTA c takes the c-th of G equal
+// shares of that sequence, whatever the lengths; a unit that crosses a border is
+// cut into pieces there, at most two per CTA.  The lengths
 // are on the device: every CTA adds the requests' block counts up itself (they
 // come from L2) and finds its first block, which costs about as much as reading
 // them once and saves a launch.
@@ -77,10 +77,16 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
   return r;
 }
 
+// What a unit costs beside its key blocks, in blocks: its query tile, its table
+// entries, its output.  Without it CTAs with many short units finish last (128
+// requests of up to 500 keys: 70 us against 60; longer ones do not notice).
+constexpr int kUnitCost = 2;
+
 struct Tile {
   int row0, tokens, p_first, p_last;           // positions of its first and last token
   int lo, sinks;                               // its tokens see [0, sinks) and [lo, p_last]
   int sink_blocks, blocks;                     // blocks before block lo / 128, blocks in all
+  __device__ __forceinline__ int cost() const { return kUnitCost + blocks; }
 };
 
 __device__ __forceinline__ Tile make_tile(const Params& p, const Req& r, int tile) {
@@ -129,10 +135,11 @@ static_assert(sizeof(Seg) == 64, "segments are copied as four uint4");
 
 constexpr int kSegRing = 8;
 
-struct Start {                                 // where a CTA's share begins
-  long long first, end, total;                 // block numbers; total = all blocks
+struct Start {                                 // a CTA's share, and where the walk stands
+  long long first, end, total;                 // the share; the step's whole cost
+  long long unit;                              // where the current unit begins
   int ctas;                                    // CTAs that have a share
-  int b, g, tile, k;
+  int b, g, tile;
 };
 
 struct SchedSmem {
@@ -171,13 +178,13 @@ __device__ __forceinline__ Req shfl_req(const Req& r, int src) {
   return o;
 }
 
-// Blocks of one kv head of the lane's request.  Lanes with few tiles add theirs
+// Cost of one kv head of the lane's request.  Lanes with few tiles add theirs
 // up alone; a request of many tiles is shared by the warp.
-__device__ __forceinline__ long long head_blocks(const Params& p, const Req& r, int lane) {
+__device__ __forceinline__ long long head_cost(const Params& p, const Req& r, int lane) {
   const int T = n_tiles(p, r);
   long long w = 0;
   if (T <= 4)
-    for (int t = 0; t < T; ++t) w += make_tile(p, r, t).blocks;
+    for (int t = 0; t < T; ++t) w += make_tile(p, r, t).cost();
   unsigned many = __ballot_sync(0xffffffffu, T > 4);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -185,7 +192,7 @@ __device__ __forceinline__ long long head_blocks(const Params& p, const Req& r, 
     const Req q = shfl_req(r, src);
     const int Tq = n_tiles(p, q);
     long long s = 0;
-    for (int t = lane; t < Tq; t += 32) s += make_tile(p, q, t).blocks;
+    for (int t = lane; t < Tq; t += 32) s += make_tile(p, q, t).cost();
     s = warp_sum_ll(s);
     if (lane == src) w = s;
   }
@@ -207,18 +214,18 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
     if (base + lane < p.B) r = load_req(p, base + lane, &bad);
     if (bad) raise_status(p.status, KS_ERR_INVALID_ARG);
     // lanes past r1 hold another warp's requests, which the walk may come to
-    const long long w = head_blocks(p, base + lane < r1 ? r : Req{0, 0, 0}, lane) * p.Hkv;
+    const long long w = head_cost(p, base + lane < r1 ? r : Req{0, 0, 0}, lane) * p.Hkv;
     if (base == r0) {
       r_first = r;
       w_first = w;
     }
     mine += warp_sum_ll(w);
   }
-  if (lane == 0) sm.warp_sum[warp] = mine;
   if (threadIdx.x == 0) {
-    sm.start.first = sm.start.end = 0;
+    sm.start.unit = sm.start.end = 0;
     sm.published = 0;
   }
+  if (lane == 0) sm.warp_sum[warp] = mine;
   __syncthreads();
   long long total = 0, before = 0;
 #pragma unroll
@@ -239,7 +246,7 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
       bool bad;
       r = Req{0, 0, 0};
       if (base + lane < p.B) r = load_req(p, base + lane, &bad);
-      w = head_blocks(p, base + lane < r1 ? r : Req{0, 0, 0}, lane) * p.Hkv;
+      w = head_cost(p, base + lane < r1 ? r : Req{0, 0, 0}, lane) * p.Hkv;
     }
     const long long upto = at + warp_scan_ll(w, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, first < upto);
@@ -254,15 +261,15 @@ __device__ __forceinline__ void locate(const Params& p, SchedSmem& sm) {
     const int g = (int)quotient(off, head), T = n_tiles(p, q);
     long long rest = off - g * head;
     for (int t0 = 0; t0 < T; t0 += 32) {
-      const long long nb = t0 + lane < T ? make_tile(p, q, t0 + lane).blocks : 0;
+      const long long nb = t0 + lane < T ? make_tile(p, q, t0 + lane).cost() : 0;
       const long long s = warp_scan_ll(nb, lane);
       const unsigned in = __ballot_sync(0xffffffffu, rest < s);
       if (in) {
         const int l = __ffs(in) - 1;
-        const int k = (int)(rest - __shfl_sync(0xffffffffu, s - nb, l));
+        const long long in_unit = rest - __shfl_sync(0xffffffffu, s - nb, l);
         sm.held[lane] = r;                     // the walk begins with these requests
         if (lane == 0) {
-          sm.start = Start{first, end, total, ctas, base + src, g, t0 + l, k};
+          sm.start = Start{first, end, total, first - in_unit, ctas, base + src, g, t0 + l};
           sm.base = base;
         }
         return;
@@ -292,7 +299,8 @@ __device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volat
   if (!KS_PAGED_WAIT(sm.empty[slot], ((n / kSegRing) & 1) ^ 1)) return nullptr;
   Seg* seg = &sm.seg[slot];
   Start& st = sm.start;
-  const bool over = st.first >= st.end || st.b >= p.B;
+  // block x of a unit that begins at u lies at u + kUnitCost + x
+  const bool over = st.unit + kUnitCost >= st.end || st.b >= p.B;
   bool next_request = false;
   if (lane == 0) {
     sm.published = n + 1;
@@ -301,8 +309,9 @@ __device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volat
     } else {
       const Req r = sm.held[st.b - sm.base];
       const Tile t = make_tile(p, r, st.tile);
-      const long long at = st.first;
-      const int k = st.k, nb = (int)(st.end - at < t.blocks - k ? st.end - at : t.blocks - k);
+      const long long x0 = st.unit + kUnitCost;
+      const int k = (int)max(0ll, st.first - x0);
+      const int nb = (int)min((long long)t.blocks, st.end - x0) - k;
       Seg s;
       s.b = st.b;
       s.g = st.g;
@@ -326,14 +335,13 @@ __device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volat
                    ? t.sink_blocks + (t.p_last - p.window) / kBlock + 1 - b0
                    : 0;
       if (nb < t.blocks) {
-        // block x belongs to CTA ((x + 1) ctas - 1) / total
-        const long long u0 = at - k, u1 = u0 + t.blocks;
-        s.first_cta = (int)quotient((u0 + 1) * st.ctas - 1, st.total);
-        s.pieces = (int)quotient(u1 * st.ctas - 1, st.total) - s.first_cta + 1;
+        // position y belongs to CTA ((y + 1) ctas - 1) / total
+        const long long x1 = x0 + t.blocks;
+        s.first_cta = (int)quotient((x0 + 1) * st.ctas - 1, st.total);
+        s.pieces = (int)quotient(x1 * st.ctas - 1, st.total) - s.first_cta + 1;
       }
       *seg = s;
-      st.first = at + nb;
-      st.k = 0;
+      st.unit += t.cost();
       if (++st.tile == n_tiles(p, r)) {
         st.tile = 0;
         if (++st.g == p.Hkv) {

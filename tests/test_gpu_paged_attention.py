@@ -279,6 +279,18 @@ def test_bad_pages_and_lengths_are_reported(ws):
     assert st.item() == 0 and torch.equal(out, good)
 
 
+def test_a_table_without_columns(ws):
+    """No position fits: every token sees nothing, and the lengths are reported."""
+    q = torch.randn(3, 8, 64, device="cuda").to(P.BF16)
+    out = torch.full_like(q, -3.0)
+    kp = torch.randn(2, 16, 2, 64, device="cuda").to(P.BF16)
+    i32 = lambda x: torch.tensor(x, dtype=I32, device="cuda")
+    st = i32([0])
+    B.paged_attention_bf16(q, kp, kp.clone(), torch.zeros(2, 0, dtype=I32, device="cuda"), i32([0, 1, 3]),
+                           i32([1, 2]), 2, out, ws, status=st)
+    assert (out == 0).all() and st.item() == 1
+
+
 @pytest.mark.parametrize("new,fill", [(1, 0x7F), (1, 0xFF), (60, 0x7F)])
 def test_a_workspace_that_does_not_start_out_zero_is_reported(new, fill):
     L = P.Layout([(9000, new)], 64)            # long enough to be cut into pieces
