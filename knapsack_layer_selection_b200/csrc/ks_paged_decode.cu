@@ -70,8 +70,11 @@ struct Tail {
   uint64_t esync, drain[2];                               // meetings of the output warps; MMA drains
   uint32_t tmem_base;
   int abort, last;
-  alignas(16) float nref[64], alpha[64];                  // -reference and rescale factor by row
-  float wmax[4][64];                                      // by warp and row
+  // each softmax group's own, by its rows of the piece: the groups do not wait for each other, and
+  // the next piece may divide its rows between them differently
+  struct alignas(16) {
+    float nref[32], alpha[32], wmax[4][32];               // -reference, rescale factor, maxima by warp
+  } refs[2];
   float lsum[2][4][64], ref[2][64];                       // a finished piece's, by its parity
 };
 constexpr int kTailBytes = (int)((sizeof(Tail) + 255) / 256 * 256);
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // byte of this key in a row of P: 64-key panel, and the swizzled 16-byte chunk of row e % 8
     const uint32_t p_key = (key >> 6) * row_panel + (key & 7) * 2;
     const uint32_t p_chunk = (key & 63) >> 3;
+    auto& refs = tail->refs[G];
     SegReader rd;
     uint32_t j = 0;
     bool ok = true;
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c < nch)
 #pragma unroll
                   for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<float4*>(&tail->wmax[q4][r0 + c * 8 + e]) = make_float4(
+                    *reinterpret_cast<float4*>(&refs.wmax[q4][c * 8 + e]) = make_float4(
                         sc[c * 8 + e], sc[c * 8 + e + 1], sc[c * 8 + e + 2], sc[c * 8 + e + 3]);
             }
             if (!meet()) {
@@ -417,10 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             if (key < nch * 8) {
-              const int r = r0 + key;
-              const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
-                                           fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
-              tail->nref[r] = -fmaxf(mx, kNoRef);
+              const float mx = sl2 * fmaxf(fmaxf(refs.wmax[0][key], refs.wmax[1][key]),
+                                           fmaxf(refs.wmax[2][key], refs.wmax[3][key]));
+              refs.nref[key] = -fmaxf(mx, kNoRef);
             }
             if (!meet()) {
               ok = false;
@@ -432,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NCH; ++c)
             if (c < nch) {
-              const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-              const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+              const float4 n0 = *reinterpret_cast<const float4*>(&refs.nref[c * 8]);
+              const float4 n1 = *reinterpret_cast<const float4*>(&refs.nref[c * 8 + 4]);
               const float* x = &sc[c * 8];
               const float m0 =
                   fmax3(fmaf(x[0], sl2, n0.x), fmaf(x[1], sl2, n0.y), fmaf(x[2], sl2, n0.z));
@@ -459,20 +462,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const float w = warp_max(sc[c]);
                   if (lane == c - c0) m = w;
                 }
-              if (c0 + lane < nch * 8) tail->wmax[q4][r0 + c0 + lane] = m;
+              if (c0 + lane < nch * 8) refs.wmax[q4][c0 + lane] = m;
             }
             if (!meet()) {
               ok = false;
               break;
             }
             if (key < nch * 8) {
-              const int r = r0 + key;
-              const float mx = sl2 * fmaxf(fmaxf(tail->wmax[0][r], tail->wmax[1][r]),
-                                           fmaxf(tail->wmax[2][r], tail->wmax[3][r]));
-              const float old = -tail->nref[r];
+              const float mx = sl2 * fmaxf(fmaxf(refs.wmax[0][key], refs.wmax[1][key]),
+                                           fmaxf(refs.wmax[2][key], refs.wmax[3][key]));
+              const float old = -refs.nref[key];
               const bool up = mx - old > kStale;
-              tail->alpha[r] = up ? ex2(old - mx) : 1.0f;
-              tail->nref[r] = up ? -mx : -old;
+              refs.alpha[key] = up ? ex2(old - mx) : 1.0f;
+              refs.nref[key] = up ? -mx : -old;
             }
             if (!meet()) {
               ok = false;
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   reg_fence8(v);
 #pragma unroll
                   for (int e = 0; e < 8; ++e) {
-                    const float a = tail->alpha[r0 + c * 8 + e];
+                    const float a = refs.alpha[c * 8 + e];
                     v[e] *= a;
                     l[c * 8 + e] *= a;
                   }
@@ -512,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NCH; ++c)
             if (c < nch) {
-              const float4 n0 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8]);
-              const float4 n1 = *reinterpret_cast<const float4*>(&tail->nref[r0 + c * 8 + 4]);
+              const float4 n0 = *reinterpret_cast<const float4*>(&refs.nref[c * 8]);
+              const float4 n1 = *reinterpret_cast<const float4*>(&refs.nref[c * 8 + 4]);
               const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float w = warp_sum8(&l[c * 8], lane);
           if ((lane & 3) == 0) tail->lsum[par][q4][r0 + c * 8 + (lane >> 2)] = w;
         }
-      if (key < nch * 8) tail->ref[par][r0 + key] = -tail->nref[r0 + key];
+      if (key < nch * 8) tail->ref[par][r0 + key] = -refs.nref[key];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail->l_full[par]));
       rd.release(tail->sched);

@@ -106,6 +106,27 @@ def test_row_counts_around_the_tile_sizes(heads, new, hd, ws):
         assert st.item() == 0
 
 
+@pytest.mark.parametrize("hd,grp,hi,window", [(64, 4, 11, 769), (64, 4, 14, 0), (128, 4, 11, 0), (64, 1, 60, 300),
+                                              (128, 7, 9, 0)])
+def test_many_short_requests_of_different_row_counts(hd, grp, hi, window, ws):
+    """Units of 1 to 64 rows that follow one another on the same SM: nothing of one
+    unit's rows may reach the next one's, however far its warps have run ahead."""
+    for seed in range(6):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda lo, h, n: torch.randint(lo, h + 1, (n,), generator=g).tolist()
+        lens = [(c if c > 60 else 0, n) for c, n in zip(r(0, 1300, 110), r(0, hi, 110))]
+        L = P.Layout(lens, 32, seed=seed)
+        kp, vp = L.pool(2, hd, seed=seed), L.pool(2, hd, seed=seed + 50)
+        q = _queries(L, 2 * grp, hd, seed=seed)
+        ref = P.attention_reference(L, q, kp, vp, window, 4)
+        first = None
+        for _ in range(3):
+            out, st = _attend(L, q, kp, vp, ws, window, 4, max_new=64 // grp)
+            _within(out, *ref)
+            assert st.item() == 0 and (first is None or torch.equal(out, first))
+            first = out
+
+
 @pytest.mark.parametrize("page", [8, 40, 56, 96, 128, 384, 1024])
 @pytest.mark.parametrize("new", [3, 70])
 def test_page_sizes(page, new, ws):
