@@ -27,7 +27,7 @@
 // warpgroup (REGS_LOW) to the softmax warpgroups (REGS_HIGH), whose shares add up to the
 // launch's allocation; the host refuses a build of another register count.
 // Measured: two chunks of up to 2,047 tokens over 8,192 cached keys (32/8 heads of
-// 128, 550 GFLOP) 475 us alone, 1.16 PFLOP/s; 8 requests of 72 rows over up to
+// 128, 550 GFLOP) 470 us back to back, 1.17 PFLOP/s; 8 requests of 72 rows over up to
 // 16,384 keys 98 us, where the few-row kernel's 128-column form took 354.
 #include <algorithm>
 
