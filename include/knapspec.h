@@ -359,8 +359,10 @@ KS_API ks_status ks_rope_append_bf16(const void* q, int64_t q_stride, const void
  * Between tokens of one request the values must be finite: a key that one token
  * sees enters the other tokens' sums with weight zero.
  * A page id outside the pool counts as a page of zeros and, like a request
- * whose lengths break max_new, n_tokens or max_blocks (its excess is dropped),
- * puts KS_ERR_INVALID_ARG in status.
+ * whose lengths break max_new, n_tokens or max_blocks, puts KS_ERR_INVALID_ARG
+ * in status.  Of such a request the tokens past max_new or n_tokens are left out
+ * (their rows as they are) and so are the keys past its table row; its other
+ * tokens keep their positions kv_len[b] - new .. and see what is left.
  * workspace: device, 256-byte aligned, ks_paged_attention_workspace_size()
  * bytes, zero before its first use; every call leaves it fit for the next one
  * (of any shape), so it needs no clearing again unless status reports

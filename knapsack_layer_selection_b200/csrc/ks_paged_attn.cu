@@ -33,7 +33,7 @@ ks_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t st) {
   p.n_slots = pool.n_pages * pool.page_size;
   p.box = std::min(paged::kBlock, pool.page_size & -pool.page_size);
   while (p.box << p.log2_boxes < paged::kBlock) ++p.log2_boxes;
-  p.window = a.window < p.cap ? a.window : 0;   // a window that no position outruns hides nothing
+  p.window = a.window;
   p.sinks = a.n_sinks;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)pool.head_dim));
   // Up to 64 rows the keys' traffic bounds a step and the few-row kernel is the faster (64 rows:

@@ -314,10 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&tail->s_free[G]));   // S_{i+2} may be computed now
         if (i < lead || i >= trail) {
           const int kb = s.key_block(i - i0);
-          // a row sees keys up to its position that are in its window or among the first;
-          // as ranges of this block: e <= last, and e >= wlo or e < sinks
+          // a row sees keys of the table up to its position that are in its window or among the
+          // first; as ranges of this block: e <= last, and e >= wlo or e < sinks
           const int key0 = kb * C::BN;
-          const int pos = s.p_first + rt, last = pos - key0;
+          const int pos = s.p_first + rt, last = min(pos, s.last_key) - key0;
           const int wlo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - key0 : 0;
           const int sk = p.window > 0 ? p.sinks - key0 : 0;
 #pragma unroll

@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nch > 0) {
           if (i < lead || i >= trail) {
             // row r is token r / grp at p_first + r / grp: it sees key k from row (k - p_first) grp
-            // on, and while the key is in its window up to row (k - p_first + window) grp
+            // on, and while the key is in its window up to row (k - p_first + window) grp; keys past
+            // the table's row are nobody's
             const int k = s.key_block(i) * kBlock + key;
             const long long d = (long long)k - s.p_first;
             const int from = (int)(d < 0 ? 0 : d > 128 ? 128 : d) * p.grp;
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const long long e = d + p.window;
               to = (int)(e < 0 ? 0 : e > 128 ? 128 : e) * p.grp;
             }
+            if (k > s.last_key) to = 0;
 #pragma unroll
             for (int c = 0; c < CPG; ++c)
               if (r0 + c < from || r0 + c >= to) sc[c] = -INFINITY;

@@ -54,8 +54,10 @@ struct Params {
 };
 
 // A request's rows after every clamp that keeps broken lengths inside the
-// buffers; pos0 (of its first token) is negative where kv_len is shorter than
-// the chunk.
+// buffers.  pos0, the position of its first token, follows from the lengths as
+// given, so that the rows that are left keep their places whatever is dropped: it
+// is negative where kv_len is shorter than the chunk, and past the table's row
+// where kv_len is longer than that.
 struct Req {
   int row0, n, pos0;
 };
@@ -68,12 +70,11 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
   if (c0 < 0 || c0 > p.n_tokens) n = 0;
   else if (n > p.n_tokens - c0) n = p.n_tokens - c0;
   if (n < 0) n = 0;
-  const int kv = max(0, min(kv_in, p.cap));
-  *bad = n != raw || kv != kv_in;
+  *bad = n != raw || kv_in < 0 || kv_in > p.cap;
   Req r;
   r.row0 = (int)c0;
   r.n = (int)n;
-  r.pos0 = kv - (int)n;
+  r.pos0 = n > 0 ? (int)(max(0, kv_in) - raw) : 0;   // c0 >= 0 here, so raw < 2^31
   return r;
 }
 
@@ -83,8 +84,9 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, bool* bad) {
 constexpr int kUnitCost = 2;
 
 struct Tile {
-  int row0, tokens, p_first, p_last;           // positions of its first and last token
-  int lo, sinks;                               // its tokens see [0, sinks) and [lo, p_last]
+  int row0, tokens, p_first;                   // p_first: position of its first token
+  int p_end, last_key;                         // of its last token; the same inside the table's row
+  int lo, sinks;                               // its tokens see [0, sinks) and [lo, last_key]
   int sink_blocks, blocks;                     // blocks before block lo / 128, blocks in all
   __device__ __forceinline__ int cost() const { return kUnitCost + blocks; }
 };
@@ -95,13 +97,14 @@ __device__ __forceinline__ Tile make_tile(const Params& p, const Req& r, int til
   t.row0 = r.row0 + t0;
   t.tokens = min(p.tile_tokens, r.n - t0);
   t.p_first = r.pos0 + t0;
-  t.p_last = t.p_first + t.tokens - 1;
-  t.lo = p.window > 0 && t.p_first >= p.window ? t.p_first - p.window + 1 : 0;
+  t.p_end = t.p_first + t.tokens - 1;
+  t.last_key = min(t.p_end, p.cap - 1);
+  t.lo = p.window > 0 && t.p_first >= p.window ? min(t.p_first - p.window + 1, p.cap) : 0;
   t.sinks = p.window > 0 ? min(p.sinks, t.lo) : 0;
   const int b0 = t.lo / kBlock;
   t.sink_blocks = min((t.sinks + kBlock - 1) / kBlock, b0);
   // a tile whose tokens see nothing still has one (masked) block: its rows are zeros
-  t.blocks = t.sink_blocks + (t.p_last >= 0 ? t.p_last / kBlock - b0 + 1 : 1);
+  t.blocks = max(1, t.sink_blocks + (t.last_key >= 0 ? t.last_key / kBlock - b0 + 1 : 0));
   return t;
 }
 
@@ -112,7 +115,7 @@ __device__ __forceinline__ int n_tiles(const Params& p, const Req& r) {
 // One piece of a unit, as the roles of a CTA read it from the ring.
 struct alignas(16) Seg {
   int b, g, row0, tokens;
-  int p_first, p_last, lo, sinks;
+  int p_first, last_key, lo, sinks;
   int sink_blocks, k0, nb, blocks;             // blocks k0 .. k0+nb-1 of the unit's `blocks`; nb = 0 ends
   int first_cta, pieces;                       // of a cut unit (pieces = 1 otherwise)
   int lead, trail;                             // unit blocks k with some key hidden from some token:
@@ -123,12 +126,12 @@ struct alignas(16) Seg {
   }
   // Keys [j0, j1] of which no token of the tile sees any.
   __device__ __forceinline__ bool unseen(int j0, int j1) const {
-    return j0 > p_last || (j1 < lo && j0 >= sinks);
+    return j0 > last_key || (j1 < lo && j0 >= sinks);
   }
   // Some key of this block is hidden from every token.
   __device__ __forceinline__ bool ragged(int kb) const {
     const int j0 = kb * kBlock, j1 = j0 + kBlock - 1;
-    return j1 > p_last || (j0 < lo && j1 >= sinks);
+    return j1 > last_key || (j0 < lo && j1 >= sinks);
   }
 };
 static_assert(sizeof(Seg) == 64, "segments are copied as four uint4");
@@ -318,7 +321,7 @@ __device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volat
       s.row0 = t.row0;
       s.tokens = t.tokens;
       s.p_first = t.p_first;
-      s.p_last = t.p_last;
+      s.last_key = t.last_key;
       s.lo = t.lo;
       s.sinks = t.sinks;
       s.sink_blocks = t.sink_blocks;
@@ -327,12 +330,12 @@ __device__ __forceinline__ const Seg* walk(const Params& p, SchedSmem& sm, volat
       s.blocks = t.blocks;
       s.first_cta = blockIdx.x;
       s.pieces = 1;
-      // keys up to p_first are below the causal edge of every token; the window's lower edge
+      // keys up to p_first that the table holds are seen by every token; the window's lower edge
       // crosses the blocks from lo's to the one of the last token's first key
       const int b0 = t.lo / kBlock;
-      s.trail = t.p_first < 0 ? 0 : t.sink_blocks + max(0, (t.p_first + 1) / kBlock - b0);
-      s.lead = p.window > 0 && t.p_last >= p.window
-                   ? t.sink_blocks + (t.p_last - p.window) / kBlock + 1 - b0
+      s.trail = t.p_first < 0 ? 0 : t.sink_blocks + max(0, (min(t.p_first, p.cap - 1) + 1) / kBlock - b0);
+      s.lead = p.window > 0 && t.p_end >= p.window
+                   ? t.sink_blocks + (t.p_end - p.window) / kBlock + 1 - b0
                    : 0;
       if (nb < t.blocks) {
         // position y belongs to CTA ((y + 1) ctas - 1) / total
@@ -501,7 +504,7 @@ template <int PANELS>
 __device__ __forceinline__ void zero_unseen(const Params& p, const Seg& s, int kb, unsigned char* v,
                                             int lane) {
   const int j0 = kb * kBlock, up = p.box - 1;
-  const int tail = max(0, min(kBlock, s.p_last + 1 - j0));
+  const int tail = max(0, min(kBlock, s.last_key + 1 - j0));
   zero_rows<PANELS>(v, tail, min(kBlock, (tail + up) & ~up), lane);
   const int g0 = max(0, min(kBlock, s.sinks - j0)), g1 = max(0, min(kBlock, s.lo - j0));
   if (g0 < g1) {                               // the gap [g0, g1)
