@@ -366,8 +366,10 @@ KS_API ks_status ks_rope_append_bf16(const void* q, int64_t q_stride, const void
  * workspace: device, 256-byte aligned, ks_paged_attention_workspace_size()
  * bytes, zero before its first use; every call leaves it fit for the next one
  * (of any shape), so it needs no clearing again unless status reports
- * KS_ERR_TIMEOUT.  Calls that overlap need a workspace each; one that does not
- * start out zero is KS_ERR_WORKSPACE in status.
+ * KS_ERR_TIMEOUT or KS_ERR_WORKSPACE.  Calls that overlap need a workspace each.
+ * A call that finds other than zeros where it counts its pieces reports
+ * KS_ERR_WORKSPACE in status and its result is void; only counts that a call
+ * which gave up, or two that shared a workspace, left there may pass for its own.
  * Long key ranges are cut over the GPU's SMs and the pieces joined in a fixed
  * order: the same call gives the same bits, but a row's last bits depend on the
  * step's lengths.

@@ -36,7 +36,13 @@ constexpr size_t kCounterBytes = 1024;
 constexpr size_t kPieceStats = 128 * sizeof(float2);
 constexpr size_t kPieceBytes = kPieceStats + 128 * 128 * sizeof(float);
 constexpr size_t kWorkspaceBytes = kCounterBytes + 2 * kMaxCtas * kPieceBytes;
-static_assert(kMaxCtas * sizeof(int) <= kCounterBytes, "counters");
+static_assert(kMaxCtas * sizeof(uint32_t) <= kCounterBytes, "counters");
+// Arrivals are counted in steps of kArrival (odd, so it has an inverse modulo 2^32): n arrivals read
+// n kArrival, and a word that no arrivals made, a small number above all, stands for a count far past
+// any unit's pieces.  In steps of one, a leftover count c < pieces would make the unit's last arrival
+// but c join pieces that are not there yet, and be c again afterwards.
+constexpr uint32_t kArrival = 0x4164d839u, kArrivalInv = 0xc4db9609u;
+static_assert(kArrival * kArrivalInv == 1u, "inverse");
 
 struct Params {
   const int32_t *table, *cu, *kv_len;
@@ -525,13 +531,14 @@ __device__ __forceinline__ unsigned char* own_piece(const Params& p, const Seg& 
 
 // One thread, after the CTA's writers of the piece have met (its fence then covers
 // their stores too): true for the unit's last arrival.  The counter is zero again
-// afterwards.  The readers of the pieces meet it again before they read.
+// afterwards.  The readers of the pieces meet it again before they read.  A counter that
+// did not start out zero is reported by the first arrival that finds it.
 __device__ __forceinline__ bool arrive_piece(const Params& p, const Seg& s) {
-  int* counter = reinterpret_cast<int*>(p.ws) + s.first_cta;
+  uint32_t* counter = reinterpret_cast<uint32_t*>(p.ws) + s.first_cta;
   __threadfence();
-  const int old = atomicAdd(counter, 1);
-  if (old < 0 || old >= s.pieces) raise_status(p.status, KS_ERR_WORKSPACE);
-  const bool last = old == s.pieces - 1;
+  const uint32_t before = atomicAdd(counter, kArrival) * kArrivalInv, pieces = s.pieces;
+  if (before >= pieces) raise_status(p.status, KS_ERR_WORKSPACE);
+  const bool last = before == pieces - 1;
   if (last) *counter = 0;
   __threadfence();
   return last;
