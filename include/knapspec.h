@@ -318,6 +318,26 @@ KS_API ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, in
                               int32_t* status, ks_stream_t stream);
 
 /*
+ * The same where tokens are taken back: ks_page_plan holds a request's pages to
+ * be the ceil(ctx_len / page_size) that its cached tokens fill, so when ctx_len
+ * falls below a page border (a verification rejects draft tokens) the pages
+ * behind it are the caller's to give back before the next plan, which would take
+ * new ones over their entries.  Here n_held (device [B], updated in place; NULL:
+ * as ks_page_plan) counts the pages in front of row b that belong to request b:
+ * pages are taken only behind them, and a page that a rejection emptied is
+ * filled again.  A new request starts at 0; one that ends gives back the n_held
+ * pages of its row.  n_held below the cached tokens' pages or above max_blocks
+ * is KS_ERR_INVALID_ARG in status and an empty step, which leaves n_held as it
+ * was.  Repeated with the same lengths it takes no pages.
+ */
+KS_API ks_status ks_page_plan_carried(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
+                                      const int32_t* free_pages, int32_t n_free, int32_t n_pages,
+                                      int32_t page_size, int32_t* block_table, int32_t max_blocks,
+                                      int32_t max_tokens, int32_t* cu_new, int32_t* kv_len,
+                                      int32_t* positions, int32_t* slots, int32_t* n_taken,
+                                      int32_t* n_held, int32_t* status, ks_stream_t stream);
+
+/*
  * Rotary positions on a step's queries and keys, and its keys and values into
  * their pages, in one pass: with theta_j = rope_base^(-2j/head_dim) and p =
  * positions[i], q_out[i] = RoPE_p(q[i]), slot slots[i] of the pool = RoPE_p(k[i])

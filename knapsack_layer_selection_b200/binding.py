@@ -87,7 +87,7 @@ EXPORTS = ["ks_version", "ks_last_error", "ks_status_string", "ks_quantize_weigh
            "ks_workspace_status", "ks_gemm_bf16", "ks_attention_bf16",
            "ks_check_bounded_wait", "ks_lemma_workspace_size", "ks_lemma_check", "ks_eval_set",
            "ks_workspace_size_contexts", "ks_solve_contexts", "ks_page_plan",
-           "ks_rope_append_bf16", "ks_paged_attention_workspace_size", "ks_paged_attention_bf16"]
+           "ks_page_plan_carried", "ks_rope_append_bf16", "ks_paged_attention_workspace_size", "ks_paged_attention_bf16"]
 
 _lib = None
 
@@ -130,6 +130,8 @@ def load() -> ctypes.CDLL:
         "ks_solve_contexts": ([P, P, I32, P, I32, P, P, P, P, P, SZ, P, P], ctypes.c_int),
         "ks_page_plan": ([P, P, I32, P, I32, I32, I32, P, I32, I32, P, P, P, P, P, P, P],
                          ctypes.c_int),
+        "ks_page_plan_carried": ([P, P, I32, P, I32, I32, I32, P, I32, I32, P, P, P, P, P, P, P, P],
+                                 ctypes.c_int),
         "ks_rope_append_bf16": ([P, I64, P, I64, P, I64, I32, I32, P, P, P, D, P, P, P],
                                 ctypes.c_int),
         "ks_paged_attention_workspace_size": ([ctypes.POINTER(SZ)], ctypes.c_int),
@@ -424,10 +426,13 @@ def _same(t: torch.Tensor, shape: tuple, name: str) -> None:
 def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
               block_table: torch.Tensor, page_size: int, n_pages: int, cu_new: torch.Tensor,
               kv_len: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
-              n_taken: torch.Tensor, status: Optional[torch.Tensor] = None) -> None:
+              n_taken: torch.Tensor, status: Optional[torch.Tensor] = None,
+              n_held: Optional[torch.Tensor] = None) -> None:
     """A step's layout from the requests' lengths (ks_page_plan), all int32:
     ctx_len, new_len, kv_len [B], free_pages [n], block_table [B][max_blocks]
-    (updated in place), cu_new [B+1], positions, slots [max_tokens], n_taken [1]."""
+    (updated in place), cu_new [B+1], positions, slots [max_tokens], n_taken [1].
+    n_held [B] (updated in place): the pages of each row that belong to its
+    request, wanted where ctx_len may fall back (ks_page_plan_carried)."""
     row = ctx_len.shape
     if len(row) != 1:
         raise KnapSpecError(f"ctx_len must be [B], got {tuple(row)}")
@@ -442,14 +447,18 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Te
     _same(free_pages, (n_free,), "free_pages")
     _same(positions, (cap,), "positions")
     _same(slots, (cap,), "slots")
+    if n_held is not None:
+        _same(n_held, row, "n_held")
     d = _device(ctx_len)
-    _check(load().ks_page_plan(_ptr(ctx_len, _I32, "ctx_len", d), _ptr(new_len, _I32, "new_len", d),
-                               B, _ptr(free_pages, _I32, "free_pages", d), n_free, n_pages,
-                               page_size, _ptr(block_table, _I32, "block_table", d),
-                               block_table.shape[1], cap, _ptr(cu_new, _I32, "cu_new", d),
-                               _ptr(kv_len, _I32, "kv_len", d), _ptr(positions, _I32, "positions", d),
-                               _ptr(slots, _I32, "slots", d), _ptr(n_taken, _I32, "n_taken", d),
-                               _status_ptr(status, d), _stream_of(d)))
+    _check(load().ks_page_plan_carried(
+        _ptr(ctx_len, _I32, "ctx_len", d), _ptr(new_len, _I32, "new_len", d), B,
+        _ptr(free_pages, _I32, "free_pages", d), n_free, n_pages, page_size,
+        _ptr(block_table, _I32, "block_table", d), block_table.shape[1], cap,
+        _ptr(cu_new, _I32, "cu_new", d), _ptr(kv_len, _I32, "kv_len", d),
+        _ptr(positions, _I32, "positions", d), _ptr(slots, _I32, "slots", d),
+        _ptr(n_taken, _I32, "n_taken", d),
+        None if n_held is None else _ptr(n_held, _I32, "n_held", d), _status_ptr(status, d),
+        _stream_of(d)))
 
 
 def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, dev: int) -> PagePool:

@@ -19,6 +19,12 @@ struct PlanArgs {
   const int32_t *ctx_len, *new_len, *free_pages;
   int32_t *block_table, *cu_new, *kv_len, *positions, *slots, *n_taken, *status;
   int B, n_free, n_pages, page_size, max_blocks, max_tokens;
+  int32_t* n_held;                           // NULL: what the cached tokens fill
+  // pages in front of request r's row that are its own; the cached tokens fill the first of them
+  __device__ __forceinline__ int filled(long long ctx) const {
+    return (int)((ctx + page_size - 1) / page_size);
+  }
+  __device__ __forceinline__ int held(int r) const { return n_held ? n_held[r] : filled(ctx_len[r]); }
 };
 
 // Last index r of off[0 .. n] with off[r] <= i (off ascending, off[n] > i).
@@ -50,12 +56,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   bool bad = false;
   for (int b = tid; b < p.B; b += kPlanThreads) {
     const long long c = p.ctx_len[b], n = p.new_len[b];
-    const bool wrong = c < 0 || n < 0 || c + n > row_cap;
+    bool wrong = c < 0 || n < 0 || c + n > row_cap;
+    int held = 0;
+    if (!wrong) {
+      held = p.filled(c);
+      if (p.n_held) {
+        const int h = p.n_held[b];
+        wrong = h < held || h > p.max_blocks;
+        held = h;
+      }
+    }
     bad |= wrong;
     tok[b] = wrong ? 0 : (int32_t)n;
-    pag[b] = wrong ? 0
-                   : (int32_t)((c + n + p.page_size - 1) / p.page_size -
-                               (c + p.page_size - 1) / p.page_size);
+    pag[b] = wrong ? 0 : max(0, p.filled(c + n) - held);
   }
   bad = __syncthreads_or(bad);
 
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   }
   for (long long i = first; i < total_pag; i += step) {
     const int r = find_segment(pag, p.B, (int)i);
-    const int held = (int)(((long long)p.ctx_len[r] + p.page_size - 1) / p.page_size);
+    const int held = p.held(r);
     int page = p.free_pages[i];
     if ((unsigned)page >= (unsigned)p.n_pages) {
       page = -1;
@@ -136,8 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
       const int r = find_segment(tok, p.B, (int)i);
       const int ctx = p.ctx_len[r];
       pos = ctx + ((int)i - tok[r]);
-      const int held = (int)(((long long)ctx + p.page_size - 1) / p.page_size);
-      const int blk = pos / p.page_size;
+      const int held = p.held(r), blk = pos / p.page_size;
       const int page = blk < held ? p.block_table[(long long)r * p.max_blocks + blk]
                                   : p.free_pages[pag[r] + (blk - held)];
       if ((unsigned)page < (unsigned)p.n_pages) slot = page * p.page_size + (pos - blk * p.page_size);
@@ -146,6 +158,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     p.positions[i] = pos;
     p.slots[i] = slot;
   }
+}
+
+// The counts that the plan carries on, in a launch of their own: every CTA of the plan reads them all,
+// so none of them may be written there.  A refused step has kv_len = 0 and changes nothing.
+__global__ void __launch_bounds__(kPlanThreads) plan_carry_kernel(const PlanArgs p) {
+  const int b = blockIdx.x * kPlanThreads + threadIdx.x;
+  if (b >= p.B) return;
+  const int filled = p.filled(p.kv_len[b]);
+  if (filled > 0 && filled > p.n_held[b]) p.n_held[b] = filled;
 }
 
 constexpr int kAppendThreads = 256;            // at most
@@ -252,6 +273,17 @@ ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B
                        int32_t page_size, int32_t* block_table, int32_t max_blocks,
                        int32_t max_tokens, int32_t* cu_new, int32_t* kv_len, int32_t* positions,
                        int32_t* slots, int32_t* n_taken, int32_t* status, ks_stream_t stream) {
+  return ks_page_plan_carried(ctx_len, new_len, B, free_pages, n_free, n_pages, page_size, block_table,
+                              max_blocks, max_tokens, cu_new, kv_len, positions, slots, n_taken, nullptr,
+                              status, stream);
+}
+
+ks_status ks_page_plan_carried(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
+                               const int32_t* free_pages, int32_t n_free, int32_t n_pages,
+                               int32_t page_size, int32_t* block_table, int32_t max_blocks,
+                               int32_t max_tokens, int32_t* cu_new, int32_t* kv_len,
+                               int32_t* positions, int32_t* slots, int32_t* n_taken, int32_t* n_held,
+                               int32_t* status, ks_stream_t stream) {
   if (B < 0 || n_free < 0 || n_pages < 1 || page_size < 1 || max_blocks < 0 || max_tokens < 0)
     return fail(KS_ERR_INVALID_ARG, "page plan: bad size");
   if (B > kMaxRequests) return fail(KS_ERR_UNSUPPORTED, "page plan: at most 16384 requests");
@@ -273,12 +305,18 @@ ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B
     return KS_OK;
   }));
   const PlanArgs a{ctx_len, new_len, free_pages, block_table, cu_new,  kv_len,    positions,  slots,
-                   n_taken, status,  B,          n_free,      n_pages, page_size, max_blocks, max_tokens};
+                   n_taken, status,  B,          n_free,      n_pages, page_size, max_blocks, max_tokens,
+                   n_held};
   const int rows = max_tokens > B + 1 ? max_tokens : B + 1;
   const int grid = std::min(ceil_div(rows, kPlanThreads), sm_count());
-  ProfScope prof(KK_PAGE_PLAN, st, 0.0, 16.0 * B + 8.0 * max_tokens);
+  const bool carried = n_held && B;
+  ProfScope prof(KK_PAGE_PLAN, st, 0.0, 16.0 * B + 8.0 * max_tokens, carried ? 2 : 1);
   page_plan_kernel<<<grid, kPlanThreads, smem, st>>>(a);
   KS_LAUNCH_CHECK();
+  if (carried) {
+    plan_carry_kernel<<<ceil_div(B, kPlanThreads), kPlanThreads, 0, st>>>(a);
+    KS_LAUNCH_CHECK();
+  }
   return KS_OK;
 }
 
