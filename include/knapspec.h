@@ -308,7 +308,8 @@ typedef struct {
  * positions and slots -1, block_table as it was).  A page id outside
  * 0 .. n_pages-1 (in free_pages, or in the entry that holds a new token) gives
  * its tokens slot -1 and KS_ERR_INVALID_ARG; the entry then holds -1 if it
- * was taken now.
+ * was taken now.  (A list padded with such ids therefore does not run out as a
+ * short one does.)
  */
 KS_API ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
                               const int32_t* free_pages, int32_t n_free, int32_t n_pages,
@@ -318,24 +319,35 @@ KS_API ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, in
                               int32_t* status, ks_stream_t stream);
 
 /*
- * The same where tokens are taken back: ks_page_plan holds a request's pages to
- * be the ceil(ctx_len / page_size) that its cached tokens fill, so when ctx_len
- * falls below a page border (a verification rejects draft tokens) the pages
- * behind it are the caller's to give back before the next plan, which would take
- * new ones over their entries.  Here n_held (device [B], updated in place; NULL:
+ * The same with the books of the pages kept on the device, for steps that take
+ * tokens back and for a captured step that is replayed.
+ * ks_page_plan holds a request's pages to be the ceil(ctx_len / page_size) that
+ * its cached tokens fill, so when ctx_len falls below a page border (a
+ * verification rejects draft tokens) the pages behind it are the caller's to give
+ * back before the next plan, which would take new ones over their entries.  Here
+ * n_held (device [B], updated in place; NULL:
  * as ks_page_plan) counts the pages in front of row b that belong to request b:
  * pages are taken only behind them, and a page that a rejection emptied is
  * filled again.  A new request starts at 0; one that ends gives back the n_held
  * pages of its row.  n_held below the cached tokens' pages or above max_blocks
  * is KS_ERR_INVALID_ARG in status and an empty step, which leaves n_held as it
  * was.  Repeated with the same lengths it takes no pages.
+ * ks_page_plan takes pages from the front of free_pages and leaves it to the
+ * caller to cut the list by n_taken before the next step; n_free is fixed in a
+ * captured call.  Here the free pages are those from free_pages[free_start[0]] on
+ * (free_start: device [1], updated in place; NULL: from the front), and the step
+ * moves free_start past what it took, so a replay goes on where the last one
+ * stopped.  Pages are given back by moving free_start down and writing them from
+ * there.  Fewer than wanted from there to n_free is KS_ERR_WORKSPACE and an empty
+ * step; a free_start outside 0 .. n_free is KS_ERR_INVALID_ARG and one too.
  */
 KS_API ks_status ks_page_plan_carried(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
                                       const int32_t* free_pages, int32_t n_free, int32_t n_pages,
                                       int32_t page_size, int32_t* block_table, int32_t max_blocks,
                                       int32_t max_tokens, int32_t* cu_new, int32_t* kv_len,
                                       int32_t* positions, int32_t* slots, int32_t* n_taken,
-                                      int32_t* n_held, int32_t* status, ks_stream_t stream);
+                                      int32_t* n_held, int32_t* free_start, int32_t* status,
+                                      ks_stream_t stream);
 
 /*
  * Rotary positions on a step's queries and keys, and its keys and values into

@@ -130,8 +130,8 @@ def load() -> ctypes.CDLL:
         "ks_solve_contexts": ([P, P, I32, P, I32, P, P, P, P, P, SZ, P, P], ctypes.c_int),
         "ks_page_plan": ([P, P, I32, P, I32, I32, I32, P, I32, I32, P, P, P, P, P, P, P],
                          ctypes.c_int),
-        "ks_page_plan_carried": ([P, P, I32, P, I32, I32, I32, P, I32, I32, P, P, P, P, P, P, P, P],
-                                 ctypes.c_int),
+        "ks_page_plan_carried": ([P, P, I32, P, I32, I32, I32, P, I32, I32, P, P, P, P, P, P, P, P,
+                                  P], ctypes.c_int),
         "ks_rope_append_bf16": ([P, I64, P, I64, P, I64, I32, I32, P, P, P, D, P, P, P],
                                 ctypes.c_int),
         "ks_paged_attention_workspace_size": ([ctypes.POINTER(SZ)], ctypes.c_int),
@@ -427,12 +427,15 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Te
               block_table: torch.Tensor, page_size: int, n_pages: int, cu_new: torch.Tensor,
               kv_len: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
               n_taken: torch.Tensor, status: Optional[torch.Tensor] = None,
-              n_held: Optional[torch.Tensor] = None) -> None:
+              n_held: Optional[torch.Tensor] = None,
+              free_start: Optional[torch.Tensor] = None) -> None:
     """A step's layout from the requests' lengths (ks_page_plan), all int32:
     ctx_len, new_len, kv_len [B], free_pages [n], block_table [B][max_blocks]
     (updated in place), cu_new [B+1], positions, slots [max_tokens], n_taken [1].
-    n_held [B] (updated in place): the pages of each row that belong to its
-    request, wanted where ctx_len may fall back (ks_page_plan_carried)."""
+    The books on the device (ks_page_plan_carried), both updated in place:
+    n_held [B], the pages of each row that belong to its request, wanted where
+    ctx_len may fall back; free_start [1], where the free pages begin in
+    free_pages, wanted where the call is captured and replayed."""
     row = ctx_len.shape
     if len(row) != 1:
         raise KnapSpecError(f"ctx_len must be [B], got {tuple(row)}")
@@ -449,6 +452,8 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Te
     _same(slots, (cap,), "slots")
     if n_held is not None:
         _same(n_held, row, "n_held")
+    if free_start is not None:
+        _same(free_start, (1,), "free_start")
     d = _device(ctx_len)
     _check(load().ks_page_plan_carried(
         _ptr(ctx_len, _I32, "ctx_len", d), _ptr(new_len, _I32, "new_len", d), B,
@@ -457,8 +462,9 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Te
         _ptr(cu_new, _I32, "cu_new", d), _ptr(kv_len, _I32, "kv_len", d),
         _ptr(positions, _I32, "positions", d), _ptr(slots, _I32, "slots", d),
         _ptr(n_taken, _I32, "n_taken", d),
-        None if n_held is None else _ptr(n_held, _I32, "n_held", d), _status_ptr(status, d),
-        _stream_of(d)))
+        None if n_held is None else _ptr(n_held, _I32, "n_held", d),
+        None if free_start is None else _ptr(free_start, _I32, "free_start", d),
+        _status_ptr(status, d), _stream_of(d)))
 
 
 def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, dev: int) -> PagePool:

@@ -20,6 +20,7 @@ struct PlanArgs {
   int32_t *block_table, *cu_new, *kv_len, *positions, *slots, *n_taken, *status;
   int B, n_free, n_pages, page_size, max_blocks, max_tokens;
   int32_t* n_held;                           // NULL: what the cached tokens fill
+  int32_t* free_start;                       // NULL: 0
   // pages in front of request r's row that are its own; the cached tokens fill the first of them
   __device__ __forceinline__ int filled(long long ctx) const {
     return (int)((ctx + page_size - 1) / page_size);
@@ -53,7 +54,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long row_cap = (long long)p.max_blocks * p.page_size;
 
-  bool bad = false;
+  const int start = p.free_start ? *p.free_start : 0;
+  bool bad = start < 0 || start > p.n_free;
   for (int b = tid; b < p.B; b += kPlanThreads) {
     const long long c = p.ctx_len[b], n = p.new_len[b];
     bool wrong = c < 0 || n < 0 || c + n > row_cap;
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     total_pag += warp_pag[w];
   }
   const int32_t code = bad || total_tok > p.max_tokens ? KS_ERR_INVALID_ARG
-                       : total_pag > p.n_free          ? KS_ERR_WORKSPACE
+                       : total_pag > p.n_free - start  ? KS_ERR_WORKSPACE
                                                        : KS_OK;
   const bool ok = code == KS_OK;
   if (!ok) total_tok = total_pag = 0;        // an empty step
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   for (long long i = first; i < total_pag; i += step) {
     const int r = find_segment(pag, p.B, (int)i);
     const int held = p.held(r);
-    int page = p.free_pages[i];
+    int page = p.free_pages[start + i];
     if ((unsigned)page >= (unsigned)p.n_pages) {
       page = -1;
       raise_status(p.status, KS_ERR_INVALID_ARG);
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
       pos = ctx + ((int)i - tok[r]);
       const int held = p.held(r), blk = pos / p.page_size;
       const int page = blk < held ? p.block_table[(long long)r * p.max_blocks + blk]
-                                  : p.free_pages[pag[r] + (blk - held)];
+                                  : p.free_pages[start + pag[r] + (blk - held)];
       if ((unsigned)page < (unsigned)p.n_pages) slot = page * p.page_size + (pos - blk * p.page_size);
       else raise_status(p.status, KS_ERR_INVALID_ARG);
     }
@@ -161,10 +163,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
 }
 
 // The counts that the plan carries on, in a launch of their own: every CTA of the plan reads them all,
-// so none of them may be written there.  A refused step has kv_len = 0 and changes nothing.
+// so none of them may be written there.  A refused step has kv_len = 0 and n_taken = 0 and changes
+// nothing.
 __global__ void __launch_bounds__(kPlanThreads) plan_carry_kernel(const PlanArgs p) {
   const int b = blockIdx.x * kPlanThreads + threadIdx.x;
-  if (b >= p.B) return;
+  if (b == 0 && p.free_start) *p.free_start += *p.n_taken;
+  if (b >= p.B || !p.n_held) return;
   const int filled = p.filled(p.kv_len[b]);
   if (filled > 0 && filled > p.n_held[b]) p.n_held[b] = filled;
 }
@@ -275,7 +279,7 @@ ks_status ks_page_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B
                        int32_t* slots, int32_t* n_taken, int32_t* status, ks_stream_t stream) {
   return ks_page_plan_carried(ctx_len, new_len, B, free_pages, n_free, n_pages, page_size, block_table,
                               max_blocks, max_tokens, cu_new, kv_len, positions, slots, n_taken, nullptr,
-                              status, stream);
+                              nullptr, status, stream);
 }
 
 ks_status ks_page_plan_carried(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
@@ -283,7 +287,7 @@ ks_status ks_page_plan_carried(const int32_t* ctx_len, const int32_t* new_len, i
                                int32_t page_size, int32_t* block_table, int32_t max_blocks,
                                int32_t max_tokens, int32_t* cu_new, int32_t* kv_len,
                                int32_t* positions, int32_t* slots, int32_t* n_taken, int32_t* n_held,
-                               int32_t* status, ks_stream_t stream) {
+                               int32_t* free_start, int32_t* status, ks_stream_t stream) {
   if (B < 0 || n_free < 0 || n_pages < 1 || page_size < 1 || max_blocks < 0 || max_tokens < 0)
     return fail(KS_ERR_INVALID_ARG, "page plan: bad size");
   if (B > kMaxRequests) return fail(KS_ERR_UNSUPPORTED, "page plan: at most 16384 requests");
@@ -306,15 +310,15 @@ ks_status ks_page_plan_carried(const int32_t* ctx_len, const int32_t* new_len, i
   }));
   const PlanArgs a{ctx_len, new_len, free_pages, block_table, cu_new,  kv_len,    positions,  slots,
                    n_taken, status,  B,          n_free,      n_pages, page_size, max_blocks, max_tokens,
-                   n_held};
+                   n_held,  free_start};
   const int rows = max_tokens > B + 1 ? max_tokens : B + 1;
   const int grid = std::min(ceil_div(rows, kPlanThreads), sm_count());
-  const bool carried = n_held && B;
+  const bool carried = (n_held && B) || free_start;
   ProfScope prof(KK_PAGE_PLAN, st, 0.0, 16.0 * B + 8.0 * max_tokens, carried ? 2 : 1);
   page_plan_kernel<<<grid, kPlanThreads, smem, st>>>(a);
   KS_LAUNCH_CHECK();
   if (carried) {
-    plan_carry_kernel<<<ceil_div(B, kPlanThreads), kPlanThreads, 0, st>>>(a);
+    plan_carry_kernel<<<std::max(1, ceil_div(B, kPlanThreads)), kPlanThreads, 0, st>>>(a);
     KS_LAUNCH_CHECK();
   }
   return KS_OK;
