@@ -389,7 +389,8 @@ KS_API ks_status ks_rope_append_bf16(const void* q, int64_t q_stride, const void
  * read (their entries may hold anything), nor does what a page holds at
  * positions that no token of the request sees, NaN included, reach a result.
  * Between tokens of one request the values must be finite: a key that one token
- * sees enters the other tokens' sums with weight zero.
+ * sees enters the other tokens' sums with weight zero.  Scores may be up to 2^30
+ * in size; from 2^32 on a row comes out NaN or zero.
  * A page id outside the pool counts as a page of zeros and, like a request
  * whose lengths break max_new, n_tokens or max_blocks, puts KS_ERR_INVALID_ARG
  * in status.  Of such a request the tokens past max_new or n_tokens are left out

@@ -34,12 +34,16 @@
 // The softmax reference of a row is kept until a score exceeds it by 2^24, so a
 // block needs no maximum: each thread only compares, one vote of the group finds
 // the rare block that moves a reference, and only then are maxima taken over the
-// keys and O rescaled; a piece begins with the largest score of four keys.  Row
-// sums stay with the keys' threads in fp32 and are added up once per piece; P is
-// rounded to bf16 for the tensor core, O is fp32.
+// keys and O rescaled; a piece begins with the largest score of four keys.  An
+// exponent is one fma, score * scale - reference, so it is off by the reference's
+// rounding (2^-25 of it, the same for all of a row's keys): scores up to 2^30 cost
+// nothing, from 2^32 on 2^that would leave fp32.  Row sums stay with the keys'
+// threads in fp32 and are added up once per piece; P is rounded to bf16 for the
+// tensor core, O is fp32.
 // Measured: 64 requests of one token (32/8 heads of 128, up to 8,192 keys, 1.06 GB)
-// 171 us, 6.2 TB/s of the 6.47 of a copy; 32 requests of up to 44 rows, 0.52 GB,
-// 106 us.
+// 173 us, 6.1 TB/s of the 6.47 of a copy; 32 requests of up to 44 rows, 0.52 GB,
+// 106 us.  Heads of 64 move half the bytes a block at the same work per block: the 64
+// requests, 530 MB, 139 us.
 #include <algorithm>
 
 #include "ks_paged_sched.cuh"

@@ -100,6 +100,29 @@ def _reference_row(q, k, v, pos, cap, window, sinks):
     return o, tol
 
 
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("size", [20, 29, 30])
+def test_scores_up_to_two_to_the_thirty(size, new, ws):
+    """Equal scores of 1 and -1 times 2^size: every key weighs the same (fp32 sums of at most 240 values, one
+    rounding of the weights and one of the result)."""
+    L = P.Layout([(200, new)], 16)
+    kp, vp = L.pool(1, 64, fill=0.0), L.pool(1, 64, seed=2)
+    q = torch.zeros(L.n_tokens, 2, 64, dtype=P.BF16, device="cuda")
+    q[..., 0] = 2.0 ** 10
+    v = vp[torch.tensor(L.rows[0][: P.ceil(L.kv[0], 16)], device="cuda")].flatten(0, 1)[:, 0].double()
+    seen = torch.arange(L.kv[0], device="cuda")[None] <= torch.arange(200, L.kv[0], device="cuda")[:, None]
+    w = seen.double() / seen.sum(-1, keepdim=True)
+    ref, size_of_v = w @ v[: L.kv[0]], w @ v[: L.kv[0]].abs()
+    e = P.HALF_STEP + 2.0 ** -16
+    tol = P.HALF_STEP * ref.abs() * (1 + 2 * P.HALF_STEP) + e / (1 - e) * (size_of_v + ref.abs()) + 1e-30
+    for sign in (1, -1):
+        kp[..., 0] = sign * 2.0 ** (size - 10) * 8     # sqrt(head_dim) = 8
+        out, st = _attend(q, kp, vp, L.table, L.cu, L.kv_len, new, ws)
+        assert st == 0
+        for h in range(2):
+            _within(out[:, h], ref, tol)
+
+
 # (page, columns of the table, cached tokens, new tokens, window, sinks): the table's row ends inside a
 # block of 128 keys, at its border, before the first new token, inside the window, before it
 PAST = [(16, 5, 70, 6, 0, 0), (16, 5, 70, 40, 0, 0), (128, 1, 100, 60, 0, 0), (64, 2, 128, 3, 0, 0),
