@@ -36,9 +36,10 @@ ks_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t st) {
   p.window = a.window;
   p.sinks = a.n_sinks;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)pool.head_dim));
-  // Up to 64 rows the keys' traffic bounds a step and the few-row kernel is the faster (64 rows:
-  // 395 us against the chunk kernel's 400 over 2.5 GB of keys, 16 rows 373); above, its scores no
-  // longer fit the registers.
+  // Up to 64 rows the keys' traffic bounds a step and the few-row kernel is the faster; above, its
+  // scores no longer fit the registers.  64 requests over up to 8,192 keys, 8 kv heads, few-row and
+  // chunk kernel in us: heads of 128, 4 rows 170 and 184, 32 rows 178 and 196, 64 rows 189 and 204;
+  // heads of 64, 4 rows 139 and 161, 32 rows 149 and 167, 64 rows 173 and 175.
   const bool few = (long long)p.grp * p.max_new <= 64;
   p.tile_tokens = few ? p.max_new : paged::kTileRows / p.grp;
   // a CTA per SM, or fewer where the step cannot have as many key blocks

@@ -26,9 +26,13 @@
 // with 168 registers a thread and moves them with setmaxnreg from the first
 // warpgroup (REGS_LOW) to the softmax warpgroups (REGS_HIGH), whose shares add up to the
 // launch's allocation; the host refuses a build of another register count.
+// Rounding: P is bf16 for the tensor core, and the row sums are of the rounded values
+// (in fp32), so that what rounding adds to a weight it adds to the sum too; S, O and
+// references are fp32 (2.3e-3 from fp64 in all, 1.7e-3 of it the output's own rounding).
 // Measured: two chunks of up to 2,047 tokens over 8,192 cached keys (32/8 heads of
-// 128, 550 GFLOP) 470 us back to back, 1.17 PFLOP/s; 8 requests of 72 rows over up to
-// 16,384 keys 98 us, where the few-row kernel's 128-column form took 354.
+// 128, 550 GFLOP) 546 us among other work (1.01 PFLOP/s), 465 back to back (1.18); 8
+// requests of 72 rows over up to 16,384 keys 102 and 96 us, where the few-row kernel's
+// 128-column form took 354.
 #include <algorithm>
 
 #include "ks_paged_sched.cuh"
